@@ -286,6 +286,96 @@ SSA_API ssa_status_t ssa_backward(ssa_plan_t plan, const void* q, const void* k,
                           int32_t head_dim, ssa_dtype_t dtype, int32_t topk, void* dq, void* dk,
                           void* dv, void* stream);
 
+/*
+ * Rotary positions of ssa_rotary. Channel pairs of the first `dim` channels of a head turn by the
+ * token's voxel coordinates; the other channels pass through. The dim / 2 pairs go to the axes x, y,
+ * z in this order: c = 2*floor(dim/6) channels to each of y and z, the rest to x. The j-th pair of an
+ * axis of w channels has the frequency f = theta^(-2j/w), changed by the scaling for a grid `scale`
+ * times the one the weights were trained on:
+ *   none    f
+ *   linear  f / scale
+ *   ntk     (theta * scale^(w/(w-2)))^(-2j/w): the lowest frequency is divided by the scale, the highest
+ *           kept (w = 2: kept)
+ *   yarn    f * (g + (1-g) / scale), g = clamp((extent*f/(2 pi) - beta_slow) / (beta_fast - beta_slow),
+ *           0, 1): pairs that turn more than beta_fast times over the trained extent keep their
+ *           frequency, those below beta_slow times are divided by the scale
+ * Pair p is channels (2p, 2p+1) in the interleaved layout (the one of ssa_forward_prologue) and (p, p +
+ * dim/2) in the half layout; axis and frequency of pair p are the same in both.
+ */
+typedef enum { SSA_ROTARY_INTERLEAVED = 0, SSA_ROTARY_HALF = 1 } ssa_rotary_layout_t;
+typedef enum {
+    SSA_ROTARY_SCALE_NONE = 0,
+    SSA_ROTARY_SCALE_LINEAR = 1,
+    SSA_ROTARY_SCALE_NTK = 2,
+    SSA_ROTARY_SCALE_YARN = 3
+} ssa_rotary_scaling_t;
+typedef struct {
+    double theta;       /* base, > 1 */
+    double scale;       /* > 0, grid extent over the trained one; read when scaling != none */
+    double extent;      /* trained grid extent, > 0, and 0 <= beta_slow < beta_fast: read by yarn only */
+    double beta_slow;
+    double beta_fast;
+    float mscale;       /* factor on the rotated channels, > 0 (1 = a rotation) */
+    int32_t dim;        /* rotated channels, even, 2..head_dim; 0 = head_dim */
+    int32_t layout;     /* ssa_rotary_layout_t */
+    int32_t scaling;    /* ssa_rotary_scaling_t */
+} ssa_rotary_t;
+
+/* A [N, heads, head_dim] view: element (i, h, d) at data[i*token_stride + h*head_stride + d] (strides in
+ * elements), e.g. the queries inside a fused projection's output. */
+typedef struct {
+    void* data;             /* device */
+    int64_t token_stride;
+    int64_t head_stride;
+    int32_t heads;
+} ssa_heads_t;
+
+/*
+ * Axis (0, 1, 2) and angular frequency of every rotated pair, as ssa_rotary uses them. Host only: needs
+ * no device. axis: int32 [dim/2], freq: double [dim/2] (either may be NULL).
+ * Errors: SSA_ERR_INVALID_ARG, SSA_ERR_UNSUPPORTED (head_dim outside the supported set).
+ */
+SSA_API ssa_status_t ssa_rotary_frequencies(const ssa_rotary_t* rotary, int32_t head_dim, int32_t* axis,
+                                            double* freq);
+
+/*
+ * The attention prologue as an operator of its own (Hi3D v1.0 pipeline page, "Stage 3: sparse flow
+ * sampling": rotary position embeddings and RMS normalisation of the self-attention queries and
+ * keys): per token and head, u = x / sqrt(mean_d x_d^2 + eps) * gamma when the weights are set, else
+ * u = x; then the rotary embedding of u at the token's voxel coordinates. fp32 arithmetic, angles
+ * reduced exactly, one rounding to the type at the end. Its outputs go to ssa_forward.
+ *   q, k:   inputs (their heads may differ; k and k_out both NULL = queries only). Strides >= 0: a zero
+ *           stride repeats a row.
+ *   q_gamma, k_gamma: device fp32 [head_dim], both or (NULL) neither; k_gamma is not read without k.
+ *   q_out, k_out: outputs, of the inputs' head counts, rows that do not overlap. An output may be its
+ *           own input (same pointer and strides); otherwise outputs share no memory with the inputs or
+ *           with one another. Views that interleave in memory are accepted when they have the same
+ *           token stride (the parts of one fused projection), else refused when their ranges meet.
+ * Queues work on `stream` and returns without waiting; allocates nothing. Runs on the plan's device.
+ * Errors: SSA_ERR_INVALID_ARG, SSA_ERR_UNSUPPORTED (head_dim), SSA_ERR_CUDA.
+ */
+SSA_API ssa_status_t ssa_rotary(ssa_plan_t plan, const ssa_heads_t* q, const ssa_heads_t* k,
+                                const float* q_gamma, const float* k_gamma, float eps,
+                                const ssa_rotary_t* rotary, int32_t head_dim, ssa_dtype_t dtype,
+                                const ssa_heads_t* q_out, const ssa_heads_t* k_out, void* stream);
+
+/*
+ * Gradients of ssa_rotary: from dq_out, dk_out (with respect to its outputs) to dq, dk (its inputs)
+ * and, when the weights are set, dq_gamma, dk_gamma (device fp32 [head_dim] each, sums over all tokens and
+ * heads; written, not added to). q and k are the forward's inputs and are read only when the weights are
+ * set (else they may be NULL). k-side pointers all NULL: queries only. dq and dk may be dq_out and dk_out
+ * themselves (or q and k); otherwise as the outputs of ssa_rotary. Fixed summation order: equal inputs give
+ * equal bits. Partial sums go to a buffer that is allocated and freed stream-ordered through the
+ * allocator. Otherwise as ssa_rotary; also SSA_ERR_ALLOC.
+ */
+SSA_API ssa_status_t ssa_rotary_backward(ssa_plan_t plan, const ssa_heads_t* dq_out,
+                                         const ssa_heads_t* dk_out, const ssa_heads_t* q,
+                                         const ssa_heads_t* k, const float* q_gamma,
+                                         const float* k_gamma, float eps, const ssa_rotary_t* rotary,
+                                         int32_t head_dim, ssa_dtype_t dtype, const ssa_heads_t* dq,
+                                         const ssa_heads_t* dk, float* dq_gamma, float* dk_gamma,
+                                         void* stream);
+
 /* Wait for `stream`, then read and clear the plan's device status word. */
 SSA_API ssa_status_t ssa_last_device_status(ssa_plan_t plan, void* stream);
 

@@ -9,7 +9,9 @@ without the built library raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 import re
 from typing import Optional, Sequence
@@ -52,6 +54,10 @@ _SIGS = {
                              _i32, _i32, _i32, _i32, _vp, _vp, _vp],
     "ssa_forward_ex": [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp],
     "ssa_backward": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp],
+    "ssa_rotary_frequencies": [_vp, _i32, _vp, _vp],
+    "ssa_rotary": [_vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _i32, _i32, _vp, _vp, _vp],
+    "ssa_rotary_backward": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _i32, _i32, _vp, _vp,
+                            _vp, _vp, _vp],
     "ssa_last_device_status": [_vp, _vp],
     "ssa_debug_wait_timeout": [_vp, _i64, _vp],
     "ssa_plan_destroy": [_vp],
@@ -68,6 +74,49 @@ class Options(ctypes.Structure):
     _fields_ = [("q_gamma", _vp), ("k_gamma", _vp), ("rope_theta", ctypes.c_float),
                 ("rms_eps", ctypes.c_float), ("conv_w", _vp), ("gate_w", _vp), ("gate_b", _vp),
                 ("select_share", ctypes.c_int32)]
+
+
+_LAYOUT = {"interleaved": 0, "half": 1}
+_SCALING = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class Rotary(ctypes.Structure):
+    """ssa_rotary_t (include/ssa.h): rotary positions at the voxel coordinates.
+
+    theta: base. layout: "interleaved" (pairs (2p, 2p+1)) or "half" (pairs (p, p + dim/2)). dim: rotated
+    channels (None = the whole head). scaling: "none", "linear", "ntk" or "yarn", for a grid `scale`
+    times the trained one; extent: the trained extent, with beta_slow and beta_fast, for yarn. mscale: factor on
+    the rotated channels (None = 1, for yarn 0.1 ln(scale) + 1)."""
+    _fields_ = [("theta", ctypes.c_double), ("scale", ctypes.c_double), ("extent", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("beta_fast", ctypes.c_double), ("mscale", ctypes.c_float),
+                ("dim", _i32), ("layout", _i32), ("scaling", _i32)]
+
+    def __init__(self, theta: float = 10000.0, layout: str = "interleaved", dim: Optional[int] = None,
+                 scaling: Optional[str] = None, scale: float = 1.0, extent: float = 0.0,
+                 beta_slow: float = 1.0, beta_fast: float = 32.0, mscale: Optional[float] = None):
+        if layout not in _LAYOUT:
+            raise ValueError(f"layout must be one of {sorted(_LAYOUT)}")
+        if scaling not in _SCALING:
+            raise ValueError("scaling must be none, linear, ntk or yarn")
+        if dim is not None and dim < 1:
+            raise ValueError("dim must be positive (None = the whole head)")
+        if mscale is None:
+            mscale = 0.1 * math.log(scale) + 1.0 if scaling == "yarn" and scale > 0 else 1.0
+        super().__init__(theta, scale, extent, beta_slow, beta_fast, mscale, dim or 0, _LAYOUT[layout],
+                         _SCALING[scaling])
+
+    def frequencies(self, head_dim: int):
+        """ssa_rotary_frequencies: (axis, angular frequency) of every rotated pair, as lists."""
+        n = (self.dim or head_dim) // 2
+        axis, freq = (_i32 * max(n, 1))(), (ctypes.c_double * max(n, 1))()
+        _check(lib.ssa_rotary_frequencies(ctypes.addressof(self), head_dim, axis, freq),
+               "ssa_rotary_frequencies")
+        return list(axis[:n]), list(freq[:n])
+
+
+class _Heads(ctypes.Structure):
+    """ssa_heads_t: a strided [N, heads, head_dim] view."""
+    _fields_ = [("data", _vp), ("token_stride", _i64), ("head_stride", _i64), ("heads", _i32)]
 
 
 def _load():
@@ -160,6 +209,34 @@ def _dev(t: torch.Tensor, dtype=None) -> torch.Tensor:
     return t
 
 
+def _heads(t: Optional[torch.Tensor], plan: "Plan", like: torch.Tensor):
+    """The view of a [N, heads, D] tensor of `like`'s type, device and head dimension (channels
+    contiguous), or NULL."""
+    if t is None:
+        return None
+    if t.device != plan.device or t.dtype != like.dtype:
+        raise ValueError("expected tensors of one type on the plan's device")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != plan.N or shape[2] != like.shape[2]:
+        raise ValueError("expected [N, heads, D]")
+    if stride[2] != 1:
+        raise ValueError("the channels of a head must be contiguous")
+    return _Heads(t.data_ptr(), stride[0], stride[1], shape[1])
+
+
+def _ref(s):
+    return None if s is None else ctypes.addressof(s)
+
+
+def _weights(t: Optional[torch.Tensor], n: int, like: torch.Tensor, what: str):
+    """Address of fp32 weights [n] on like's device (None = NULL)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.device != like.device or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous fp32 tensor of {n} values on the inputs' device")
+    return t.data_ptr()
+
+
 class Plan:
     """Block partition and window lists of a packed batch of voxel token sequences.
 
@@ -171,6 +248,7 @@ class Plan:
         _dev(coords, torch.int32)
         self._h = _vp()
         self.stream = stream
+        self.device = coords.device
         st = _stream(stream)
         if cu_seqlens is None:
             g = (ctypes.c_int32 * 3)(*[int(x) for x in grid])
@@ -338,6 +416,69 @@ class Plan:
                                 _DTYPE[dt], topk, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
                                 _stream(self.stream)), "ssa_backward")
         return dq, dk, dv
+
+    def _on_stream(self):
+        """Context in which results are allocated: on the plan's stream, so that their memory is
+        ordered with the kernels that write it."""
+        return contextlib.nullcontext() if self.stream is None else torch.cuda.stream(self.stream)
+
+    def _stream_of(self) -> int:
+        return (torch.cuda.current_stream(self.device) if self.stream is None else self.stream).cuda_stream
+
+    def rotary(self, q, k=None, rotary: Optional[Rotary] = None, q_gamma=None, k_gamma=None,
+               eps: float = 1e-6, q_out=None, k_out=None):
+        """ssa_rotary: RMS normalisation (when q_gamma and k_gamma, fp32 [D], are given) and rotary
+        positions of q [N, H, D] and k [N, Hk, D] at the plan's coordinates. The tensors may be strided
+        views with contiguous channels; q_out and k_out (default: new contiguous tensors) may be q and k
+        themselves. Returns (q_out, k_out), or q_out alone when k is None."""
+        rotary = Rotary() if rotary is None else rotary
+        hq, hk = _heads(q, self, q), _heads(k, self, q)
+        D = q.shape[2]
+        gq = _weights(q_gamma, D, q, "q_gamma")
+        gk = None if k is None else _weights(k_gamma, D, q, "k_gamma")
+        with self._on_stream():
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if k_out is None and k is not None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        oq, ok = _heads(q_out, self, q), _heads(k_out, self, q)
+        _check(lib.ssa_rotary(self._h, ctypes.addressof(hq), _ref(hk), gq, gk, eps,
+                              ctypes.addressof(rotary), D, _DTYPE.get(q.dtype, -1), ctypes.addressof(oq),
+                              _ref(ok), self._stream_of()), "ssa_rotary")
+        return q_out if k is None else (q_out, k_out)
+
+    def rotary_backward(self, dq_out, dk_out=None, rotary: Optional[Rotary] = None, q=None, k=None,
+                        q_gamma=None, k_gamma=None, eps: float = 1e-6, dq=None, dk=None):
+        """ssa_rotary_backward: gradients of `rotary` from those of its outputs. q and k (its inputs)
+        are needed with weights only. Returns (dq, dk), with weights (dq, dk, dq_gamma, dk_gamma); the
+        k parts are left out when dk_out is None. dq and dk may be given (dq_out and dk_out themselves
+        allowed)."""
+        rotary = Rotary() if rotary is None else rotary
+        keys = dk_out is not None
+        norm = q_gamma is not None
+        gq_, gk_ = _heads(dq_out, self, dq_out), _heads(dk_out, self, dq_out)
+        D = dq_out.shape[2]
+        gq = _weights(q_gamma, D, dq_out, "q_gamma")
+        gk = _weights(k_gamma, D, dq_out, "k_gamma") if keys else None
+        hq = _heads(q, self, dq_out) if norm else None
+        hk = _heads(k, self, dq_out) if norm and keys else None
+        wq = wk = None
+        with self._on_stream():
+            if dq is None:
+                dq = torch.empty(dq_out.shape, dtype=dq_out.dtype, device=dq_out.device)
+            if dk is None and keys:
+                dk = torch.empty(dk_out.shape, dtype=dk_out.dtype, device=dk_out.device)
+            if norm:
+                wq = torch.empty(D, dtype=torch.float32, device=dq_out.device)
+                wk = torch.empty(D, dtype=torch.float32, device=dq_out.device) if keys else None
+        oq, ok = _heads(dq, self, dq_out), _heads(dk, self, dq_out)
+        _check(lib.ssa_rotary_backward(self._h, ctypes.addressof(gq_), _ref(gk_), _ref(hq), _ref(hk), gq,
+                                       gk, eps, ctypes.addressof(rotary), D, _DTYPE.get(dq_out.dtype, -1),
+                                       ctypes.addressof(oq), _ref(ok), _ptr(wq), _ptr(wk),
+                                       self._stream_of()), "ssa_rotary_backward")
+        if keys:
+            return (dq, dk, wq, wk) if norm else (dq, dk)
+        return (dq, wq) if norm else dq
 
     def debug_wait_timeout(self, max_cycles: int):
         """ssa_debug_wait_timeout: a bounded wait that runs out on purpose (failure detection)."""
