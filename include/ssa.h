@@ -376,6 +376,47 @@ SSA_API ssa_status_t ssa_rotary_backward(ssa_plan_t plan, const ssa_heads_t* dq_
                                          const ssa_heads_t* dk, float* dq_gamma, float* dk_gamma,
                                          void* stream);
 
+/* A [N, channels] view: element (i, c) at data[i*token_stride + c]. */
+typedef struct {
+    void* data;             /* device */
+    int64_t token_stride;
+} ssa_rows_t;
+
+typedef enum { SSA_ACT_NONE = 0, SSA_ACT_SILU = 1, SSA_ACT_GELU = 2 } ssa_activation_t;
+
+/*
+ * Group normalisation of packed voxel tokens with an activation, channels last (the normalisation between
+ * the layers that produce a sparse transformer's tokens). For each sequence of the plan and each group of
+ * channels / groups consecutive channels, mean and variance (biased) over the sequence's tokens and the
+ * group's channels; sequences do not see one another. rstd = 1 / sqrt(variance + eps),
+ *   y = act((x - mean) * rstd * gamma + beta),
+ * act: none, silu z / (1 + exp(-z)), or gelu z * Phi(z) (the normal distribution function, not its tanh form).
+ *   gamma, beta: device fp32 [channels], both or (NULL) neither (1 and 0).
+ *   y: output; may be x itself (same pointer and stride), otherwise shares no memory with x.
+ *   mean, rstd: outputs, device fp32 [B, groups], both or (NULL) neither; 0 for a sequence without tokens.
+ * fp32 arithmetic, statistics merged in fp64, one rounding to the type at the end; the variance comes from
+ * deviations, not from a difference of large sums. Fixed summation order: equal inputs give equal bits. Strides
+ * >= 0 (y: >= channels). Queues work on `stream` and returns without waiting; partial sums go to a buffer that
+ * is allocated and freed stream-ordered through the allocator. Runs on the plan's device.
+ * Errors: SSA_ERR_INVALID_ARG, SSA_ERR_UNSUPPORTED (more than 65536 channels), SSA_ERR_ALLOC, SSA_ERR_CUDA.
+ */
+SSA_API ssa_status_t ssa_group_norm(ssa_plan_t plan, const ssa_rows_t* x, int32_t channels, int32_t groups,
+                                    const float* gamma, const float* beta, float eps,
+                                    ssa_activation_t activation, ssa_dtype_t dtype, const ssa_rows_t* y,
+                                    float* mean, float* rstd, void* stream);
+
+/*
+ * Gradients of ssa_group_norm: from dy (with respect to y), its input x and its mean and rstd to dx, dgamma and
+ * dbeta (device fp32 [channels], sums over all tokens; written, not added to; also without weights, as if they
+ * were 1 and 0). dx may be dy itself or x itself; otherwise it shares no memory with them. Otherwise as
+ * ssa_group_norm.
+ */
+SSA_API ssa_status_t ssa_group_norm_backward(ssa_plan_t plan, const ssa_rows_t* dy, const ssa_rows_t* x,
+                                             const float* mean, const float* rstd, int32_t channels,
+                                             int32_t groups, const float* gamma, const float* beta,
+                                             ssa_activation_t activation, ssa_dtype_t dtype,
+                                             const ssa_rows_t* dx, float* dgamma, float* dbeta, void* stream);
+
 /* Wait for `stream`, then read and clear the plan's device status word. */
 SSA_API ssa_status_t ssa_last_device_status(ssa_plan_t plan, void* stream);
 

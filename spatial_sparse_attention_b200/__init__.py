@@ -58,6 +58,8 @@ _SIGS = {
     "ssa_rotary": [_vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _i32, _i32, _vp, _vp, _vp],
     "ssa_rotary_backward": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _i32, _i32, _vp, _vp,
                             _vp, _vp, _vp],
+    "ssa_group_norm": [_vp, _vp, _i32, _i32, _vp, _vp, ctypes.c_float, _i32, _i32, _vp, _vp, _vp, _vp],
+    "ssa_group_norm_backward": [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp],
     "ssa_last_device_status": [_vp, _vp],
     "ssa_debug_wait_timeout": [_vp, _i64, _vp],
     "ssa_plan_destroy": [_vp],
@@ -76,6 +78,7 @@ class Options(ctypes.Structure):
                 ("select_share", ctypes.c_int32)]
 
 
+_ACTIVATION = {None: 0, "none": 0, "silu": 1, "gelu": 2}
 _LAYOUT = {"interleaved": 0, "half": 1}
 _SCALING = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -222,6 +225,29 @@ def _heads(t: Optional[torch.Tensor], plan: "Plan", like: torch.Tensor):
     if stride[2] != 1:
         raise ValueError("the channels of a head must be contiguous")
     return _Heads(t.data_ptr(), stride[0], stride[1], shape[1])
+
+
+class _Rows(ctypes.Structure):
+    """ssa_rows_t: a strided [N, channels] view."""
+    _fields_ = [("data", _vp), ("token_stride", _i64)]
+
+
+def _rows(t: torch.Tensor, plan: "Plan", like: torch.Tensor):
+    """The view of a [N, channels] tensor of `like`'s type, device and shape (channels contiguous)."""
+    if t.device != plan.device or t.dtype != like.dtype:
+        raise ValueError("expected tensors of one type on the plan's device")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != plan.N or shape != like.shape or shape[1] < 1:
+        raise ValueError("expected [N, channels]")
+    if stride[1] != 1 and shape[1] > 1:
+        raise ValueError("the channels of a token must be contiguous")
+    return _Rows(t.data_ptr(), stride[0])
+
+
+def _activation(name: Optional[str]) -> int:
+    if name not in _ACTIVATION:
+        raise ValueError("activation must be none, silu or gelu")
+    return _ACTIVATION[name]
 
 
 def _ref(s):
@@ -479,6 +505,48 @@ class Plan:
         if keys:
             return (dq, dk, wq, wk) if norm else (dq, dk)
         return (dq, wq) if norm else dq
+
+    def group_norm(self, x, groups: int, gamma=None, beta=None, eps: float = 1e-5,
+                   activation: Optional[str] = None, out=None, return_stats: bool = False):
+        """ssa_group_norm: group normalisation of features x [N, C] over the tokens of each packed sequence and
+        the channels of each group, weights gamma and beta (fp32 [C]) and an activation ("silu", "gelu" or none).
+        x may be a strided view with contiguous channels; out (default: a new contiguous tensor) may be x itself.
+        Returns out, or (out, mean, rstd) with the fp32 [B, groups] statistics."""
+        vx, act, C = _rows(x, self, x), _activation(activation), x.shape[1]
+        wg, wb = _weights(gamma, C, x, "gamma"), _weights(beta, C, x, "beta")
+        if groups < 1:
+            raise ValueError("groups must be positive")
+        mean = rstd = None
+        with self._on_stream():
+            if out is None:
+                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            if return_stats:
+                mean, rstd = torch.empty(2, self.batch, groups, dtype=torch.float32, device=x.device)
+        vy = _rows(out, self, x)
+        _check(lib.ssa_group_norm(self._h, ctypes.addressof(vx), C, groups, wg, wb, eps, act,
+                                  _DTYPE.get(x.dtype, -1), ctypes.addressof(vy), _ptr(mean), _ptr(rstd),
+                                  self._stream_of()), "ssa_group_norm")
+        return (out, mean, rstd) if return_stats else out
+
+    def group_norm_backward(self, dy, x, mean, rstd, groups: int, gamma=None, beta=None,
+                            activation: Optional[str] = None, dx=None):
+        """ssa_group_norm_backward: (dx, dgamma, dbeta) from the gradient of `group_norm`'s output, its input and
+        its statistics (fp32 [B, groups]). dx may be dy itself or x itself."""
+        vd, vx, act, C = _rows(dy, self, x), _rows(x, self, x), _activation(activation), x.shape[1]
+        wg, wb = _weights(gamma, C, x, "gamma"), _weights(beta, C, x, "beta")
+        if groups < 1 or mean is None or rstd is None:
+            raise ValueError("expected a positive number of groups and the forward's statistics")
+        m, r = _weights(mean, self.batch * groups, x, "mean"), _weights(rstd, self.batch * groups, x, "rstd")
+        with self._on_stream():
+            if dx is None:
+                dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            dgamma, dbeta = torch.empty(2, C, dtype=torch.float32, device=x.device)
+        vo = _rows(dx, self, x)
+        _check(lib.ssa_group_norm_backward(self._h, ctypes.addressof(vd), ctypes.addressof(vx), m, r, C, groups,
+                                           wg, wb, act, _DTYPE.get(x.dtype, -1), ctypes.addressof(vo),
+                                           dgamma.data_ptr(), dbeta.data_ptr(), self._stream_of()),
+               "ssa_group_norm_backward")
+        return dx, dgamma, dbeta
 
     def debug_wait_timeout(self, max_cycles: int):
         """ssa_debug_wait_timeout: a bounded wait that runs out on purpose (failure detection)."""

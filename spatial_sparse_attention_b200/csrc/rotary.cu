@@ -15,7 +15,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "common.cuh"
+#include "views.cuh"
 
 namespace ssa {
 
@@ -51,12 +51,6 @@ struct RotArgs {
     uint64_t turns[kMaxPairs];
     uint8_t axis[kMaxPairs];
 };
-
-template <int BYTES> struct Chunk;
-template <> struct Chunk<16> { using type = uint4; };
-template <> struct Chunk<8> { using type = uint2; };
-template <> struct Chunk<4> { using type = uint32_t; };
-template <> struct Chunk<2> { using type = uint16_t; };
 
 // How a lane's 32 bytes of a row are cut. An item is P pairs: one load of V = 2P elements (interleaved,
 // V >= 2), or two loads of V elements (half: the pairs' two sides; interleaved at V = 1). Item m of lane l
@@ -452,57 +446,6 @@ int rotary_frequencies(const ssa_rotary_t& r, int32_t D, int32_t* axis, double* 
     return p;
 }
 
-int64_t extent_of(const ssa_heads_t& v, int64_t N, int32_t D) {
-    return (N - 1) * v.token_stride + (int64_t)(v.heads - 1) * v.head_stride + D;
-}
-
-bool check_view(const ssa_heads_t* v, int64_t N, int32_t D, size_t es, bool written) {
-    if (!v || !v->data || v->heads < 1 || v->heads > 65535) return false;
-    if (v->token_stride < 0 || v->head_stride < 0) return false;
-    // the last element's offset stays inside 62 bits, products included
-    const int64_t most = (int64_t)1 << 35;
-    if ((N > 1 && v->token_stride > most) || (v->heads > 1 && v->head_stride > most)) return false;
-    if ((uintptr_t)v->data % es) return false;
-    if (written) {
-        const int64_t ts = N > 1 ? v->token_stride : INT64_MAX, hs = v->heads > 1 ? v->head_stride : INT64_MAX;
-        const bool heads_inside = hs >= D && (N == 1 || v->heads == 1 ? ts >= D : ts >= (v->heads - 1) * hs + D);
-        const bool tokens_inside = ts >= D && (N == 1 || v->heads == 1 ? hs >= D : hs >= (N - 1) * ts + D);
-        if (!heads_inside && !tokens_inside) return false;
-    }
-    return true;
-}
-
-bool same_view(const ssa_heads_t& a, const ssa_heads_t& b, int64_t N) {
-    return a.data == b.data && a.heads == b.heads && (N == 1 || a.token_stride == b.token_stride) &&
-           (a.heads == 1 || a.head_stride == b.head_stride);
-}
-
-// Whether two views share no element, as far as this can tell: their ranges do not meet, or they are
-// parts of one row of equal token stride, or of equal head stride.
-bool disjoint(const ssa_heads_t& a, const ssa_heads_t& b, int64_t N, int32_t D, size_t es) {
-    const uintptr_t pa = (uintptr_t)a.data, pb = (uintptr_t)b.data;
-    if (pa + (uintptr_t)extent_of(a, N, D) * es <= pb || pb + (uintptr_t)extent_of(b, N, D) * es <= pa) return true;
-    const int64_t d = ((int64_t)pb - (int64_t)pa) / (int64_t)es;
-    auto apart = [d](int64_t period, int64_t ea, int64_t eb) {
-        const int64_t o = ((d % period) + period) % period;
-        return o >= ea && o + eb <= period;
-    };
-    if (N > 1 && a.token_stride == b.token_stride && a.token_stride > 0 &&
-        apart(a.token_stride, (int64_t)(a.heads - 1) * a.head_stride + D, (int64_t)(b.heads - 1) * b.head_stride + D))
-        return true;
-    const int64_t s = a.head_stride;
-    return s > 0 && b.head_stride == s && (N == 1 || (a.token_stride % s == 0 && b.token_stride % s == 0)) &&
-           apart(s, D, D);
-}
-
-// Largest vector (elements) at which every row of a view starts aligned.
-int view_vector(const ssa_heads_t& v, int64_t N, size_t es, int most) {
-    while (most > 1 && ((uintptr_t)v.data % (most * es) || (N > 1 && v.token_stride % most) ||
-                        (v.heads > 1 && v.head_stride % most)))
-        most >>= 1;
-    return most;
-}
-
 template <typename T, int V, bool HALF>
 void launch_cut(const RotArgs& a, unsigned grid, bool grad, cudaStream_t st) {
     if (grad)
@@ -609,10 +552,9 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
     a.mscale = rot->mscale;
     a.sgn = backward ? -1.0f : 1.0f;
 
-    int dev = 0, sms = 148;
-    cudaGetDevice(&dev);
-    if (dev != p->device && cudaSetDevice(p->device) != cudaSuccess) return SSA_ERR_CUDA;
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, p->device);
+    const DeviceScope on(p->device);
+    if (!on.ok) return SSA_ERR_CUDA;
+    const int sms = sm_count(p->device);
     // tokens per tile: the most that still gives every SM several CTAs
     a.tile = (int)std::min<int64_t>(kMaxTile, std::max<int64_t>(1, N / (4 * sms)));
     const int64_t tiles = cdiv(N, a.tile);
@@ -640,7 +582,6 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
         }
     }
     if (out == SSA_OK && cudaGetLastError() != cudaSuccess) out = SSA_ERR_CUDA;
-    if (dev != p->device) cudaSetDevice(dev);
     return out;
 }
 

@@ -1,0 +1,121 @@
+// Strided views of caller tensors: host-side checks (alignment, overlap) and vector access, shared by
+// the operators around the attention.
+#pragma once
+
+#include <string.h>
+
+#include "common.cuh"
+
+namespace ssa {
+
+// ---- host --------------------------------------------------------------------------------------
+
+inline int64_t extent_of(const ssa_heads_t& v, int64_t N, int32_t D) {
+    return (N - 1) * v.token_stride + (int64_t)(v.heads - 1) * v.head_stride + D;
+}
+
+inline bool check_view(const ssa_heads_t* v, int64_t N, int32_t D, size_t es, bool written) {
+    if (!v || !v->data || v->heads < 1 || v->heads > 65535) return false;
+    if (v->token_stride < 0 || v->head_stride < 0) return false;
+    // the last element's offset stays inside 62 bits, products included
+    const int64_t most = (int64_t)1 << 35;
+    if ((N > 1 && v->token_stride > most) || (v->heads > 1 && v->head_stride > most)) return false;
+    if ((uintptr_t)v->data % es) return false;
+    if (written) {
+        const int64_t ts = N > 1 ? v->token_stride : INT64_MAX, hs = v->heads > 1 ? v->head_stride : INT64_MAX;
+        const bool heads_inside = hs >= D && (N == 1 || v->heads == 1 ? ts >= D : ts >= (v->heads - 1) * hs + D);
+        const bool tokens_inside = ts >= D && (N == 1 || v->heads == 1 ? hs >= D : hs >= (N - 1) * ts + D);
+        if (!heads_inside && !tokens_inside) return false;
+    }
+    return true;
+}
+
+inline bool same_view(const ssa_heads_t& a, const ssa_heads_t& b, int64_t N) {
+    return a.data == b.data && a.heads == b.heads && (N == 1 || a.token_stride == b.token_stride) &&
+           (a.heads == 1 || a.head_stride == b.head_stride);
+}
+
+// Whether two views share no element, as far as this can tell: their ranges do not meet, or they are
+// parts of one row of equal token stride, or of equal head stride.
+inline bool disjoint(const ssa_heads_t& a, const ssa_heads_t& b, int64_t N, int32_t D, size_t es) {
+    const uintptr_t pa = (uintptr_t)a.data, pb = (uintptr_t)b.data;
+    if (pa + (uintptr_t)extent_of(a, N, D) * es <= pb || pb + (uintptr_t)extent_of(b, N, D) * es <= pa) return true;
+    const int64_t d = ((int64_t)pb - (int64_t)pa) / (int64_t)es;
+    auto apart = [d](int64_t period, int64_t ea, int64_t eb) {
+        const int64_t o = ((d % period) + period) % period;
+        return o >= ea && o + eb <= period;
+    };
+    if (N > 1 && a.token_stride == b.token_stride && a.token_stride > 0 &&
+        apart(a.token_stride, (int64_t)(a.heads - 1) * a.head_stride + D, (int64_t)(b.heads - 1) * b.head_stride + D))
+        return true;
+    const int64_t s = a.head_stride;
+    return s > 0 && b.head_stride == s && (N == 1 || (a.token_stride % s == 0 && b.token_stride % s == 0)) &&
+           apart(s, D, D);
+}
+
+// Largest vector (elements) at which every row of a view starts aligned.
+inline int view_vector(const ssa_heads_t& v, int64_t N, size_t es, int most) {
+    while (most > 1 && ((uintptr_t)v.data % (most * es) || (N > 1 && v.token_stride % most) ||
+                        (v.heads > 1 && v.head_stride % most)))
+        most >>= 1;
+    return most;
+}
+
+// Makes the plan's device current for the scope.
+struct DeviceScope {
+    int before = 0;
+    bool ok = true, moved = false;
+    explicit DeviceScope(int device) {
+        if (cudaGetDevice(&before) != cudaSuccess) before = device;
+        if (before != device) {
+            moved = true;
+            ok = cudaSetDevice(device) == cudaSuccess;
+        }
+    }
+    ~DeviceScope() {
+        if (moved) cudaSetDevice(before);
+    }
+};
+
+// Multiprocessors of a device, asked once per device.
+inline int sm_count(int device) {
+    static std::atomic<int> known[64];
+    if (device >= 0 && device < 64) {
+        const int n = known[device].load(std::memory_order_relaxed);
+        if (n) return n;
+    }
+    int n = 148;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) n = 148;
+    if (device >= 0 && device < 64) known[device].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// ---- device ------------------------------------------------------------------------------------
+
+template <int BYTES> struct Chunk;
+template <> struct Chunk<16> { using type = uint4; };
+template <> struct Chunk<8> { using type = uint2; };
+template <> struct Chunk<4> { using type = uint32_t; };
+template <> struct Chunk<2> { using type = uint16_t; };
+
+// V elements of T as one load, and as floats.
+template <typename T, int V>
+struct Vec {
+    using C = typename Chunk<V * (int)sizeof(T)>::type;
+    static __device__ __forceinline__ void unpack(const C& raw, float (&e)[V]) {
+        T v[V];
+        memcpy(v, &raw, sizeof(v));
+#pragma unroll
+        for (int j = 0; j < V; ++j) e[j] = Elem<T>::to_f(v[j]);
+    }
+    static __device__ __forceinline__ C pack(const float (&e)[V]) {
+        T v[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = Elem<T>::from_f(e[j]);
+        C raw;
+        memcpy(&raw, v, sizeof(v));
+        return raw;
+    }
+};
+
+}  // namespace ssa

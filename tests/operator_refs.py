@@ -111,3 +111,110 @@ def rotary_grad(g, coords, x=None, gamma=None, eps=1e-6, **opt):
     # as the forward for every factor, and the mean of the products over the row
     bound = 96 * U * inv * (mag * np.abs(gamma) + np.abs(n) * (mag * np.abs(gamma * n)).mean(2, keepdims=True))
     return (dx, bound), ((du * n).sum((0, 1)), (mag * np.abs(n)).sum((0, 1)))
+
+
+# ---- group normalisation -------------------------------------------------------------------------
+
+def _phi(z):
+    return np.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+
+
+def _cdf(z):
+    return torch.special.ndtr(torch.from_numpy(np.ascontiguousarray(z))).numpy()
+
+
+def _sigma(z):
+    e = np.exp(-np.abs(z))
+    return np.where(z >= 0, 1 / (1 + e), e / (1 + e))
+
+
+def activation(z, name):
+    return z * _sigma(z) if name == "silu" else z * _cdf(z) if name == "gelu" else z
+
+
+def activation_grad(z, name):
+    if name == "silu":
+        return _sigma(z) * (1 + z * (1 - _sigma(z)))
+    return _cdf(z) + z * _phi(z) if name == "gelu" else np.ones_like(z)
+
+
+def activation_error(z, name):
+    """Bound, in units u, of the kernels' error of act(z) / |z| and of act'(z): sigma by a fast exponential
+    (2 + 1.2|z| ulp) and quotient (2 ulp); Phi to 5 ulp, the exponential of -z^2/2 to 2 ulp of itself and z^2 u of its
+    argument; a few operations on top. |act'| and its terms stay below 1.3 + |z|/4."""
+    if name not in ("silu", "gelu"):
+        return np.zeros_like(z)
+    return (24 + 4 * np.abs(z) + 2 * np.minimum(z * z, 30)) * (1.3 + np.abs(z) / 4)
+
+
+DEPTH = 64 + 288 + 8    # longest chain of fp32 additions: rows of a thread, row lanes of a CTA, the merge
+
+
+def norm_stats(x, cu, groups):
+    """Per (sequence, group): mean, biased variance, mean |x|, max |x - mean|."""
+    B = len(cu) - 1
+    out = np.zeros((4, B, groups))
+    for s in range(B):
+        v = x[cu[s]:cu[s + 1]].reshape(cu[s + 1] - cu[s], groups, x.shape[1] // groups)
+        if len(v):
+            m = v.mean((0, 2))
+            d = v - m[:, None]
+            out[:, s] = m, (d * d).mean((0, 2)), np.abs(v).mean((0, 2)), np.abs(d).max((0, 2))
+    return out
+
+
+def _rows_of(table, cu, C):
+    """[B, G] as [N, C]."""
+    t = np.repeat(table, C // table.shape[1], axis=1)
+    return np.concatenate([np.broadcast_to(t[s], (b - a, C)) for s, (a, b) in enumerate(zip(cu, cu[1:]))])
+
+
+def group_norm(x, cu, groups, gamma=None, beta=None, eps=1e-5, act=None):
+    """(y, bound), (mean, bound), (rstd, bound). The kernels add deviations from a pivot among the values: the mean of
+    up to 64 of them is off by 64 u of their size, at most twice the largest deviation, plus 8 u of the values;
+    the variance by the cancellation of up to 64 terms, 2 (1 + 4) times 70 u (pivots of random rows are off
+    the mean by at most 4 variances on average)."""
+    C = x.shape[1]
+    mean, var, size, most = norm_stats(x, cu, groups)
+    empty = (np.diff(cu) == 0)[:, None] | np.zeros_like(mean, bool)
+    rstd = np.where(empty, 0.0, 1 / np.sqrt(np.where(empty, 1.0, var + eps)))
+    dmean = U * (8 * size + 128 * most)
+    drstd = 360 * U * rstd
+    g = np.ones(C) if gamma is None else gamma
+    b = np.zeros(C) if beta is None else beta
+    m, r, dm = (_rows_of(t, cu, C) for t in (mean, rstd, dmean))
+    xhat = (x - m) * r
+    z = xhat * g + b
+    dz = r * np.abs(g) * (dm + U * np.abs(x)) + (360 + 6) * U * np.abs(xhat * g) + 2 * U * np.abs(b)
+    bound = 1.13 * dz + U * activation_error(z, act) * np.abs(z)
+    return (activation(z, act), bound), (mean, dmean), (rstd, drstd)
+
+
+def group_norm_grad(dy, x, mean, rstd, cu, groups, gamma=None, beta=None, act=None):
+    """(dx, bound), (dgamma, bound), (dbeta, bound) of the formula at the given statistics."""
+    N, C = x.shape
+    g = np.ones(C) if gamma is None else gamma
+    b = np.zeros(C) if beta is None else beta
+    m, r = _rows_of(mean, cu, C), _rows_of(rstd, cu, C)
+    xhat = (x - m) * r
+    exhat = U * (2 * np.abs(xhat) + (np.abs(x) + np.abs(m)) * r)
+    z = xhat * g + b
+    ez = np.abs(g) * exhat + 2 * U * (np.abs(xhat * g) + np.abs(b))
+    dz = dy * activation_grad(z, act)
+    # |act''| <= 0.8
+    edz = np.abs(dy) * ((0.8 * ez if act in ("silu", "gelu") else 0) + U * activation_error(z, act)) + U * np.abs(dz)
+    t1, e1 = dz * g, edz * np.abs(g)
+    t2, e2 = t1 * xhat, e1 * np.abs(xhat) + np.abs(t1) * exhat
+    n = np.maximum(np.diff(cu), 1)[:, None] * (C // groups)
+
+    def means(t):
+        return np.stack([t[a:c].reshape(c - a, groups, C // groups).sum((0, 2)) for a, c in zip(cu, cu[1:])]) / n
+
+    S1, S2 = _rows_of(means(t1), cu, C), _rows_of(means(t2), cu, C)
+    eS1 = _rows_of(means(e1 + DEPTH * U * np.abs(t1)), cu, C)
+    eS2 = _rows_of(means(e2 + DEPTH * U * np.abs(t2)), cu, C)
+    dx = r * (t1 - S1 - xhat * S2)
+    edx = r * (e1 + eS1 + np.abs(xhat) * eS2 + exhat * np.abs(S2) + 6 * U * (np.abs(t1) + np.abs(S1) + np.abs(xhat * S2)))
+    w = dz * xhat
+    ew = edz * np.abs(xhat) + np.abs(dz) * exhat
+    return ((dx, edx), (w.sum(0), (ew + DEPTH * U * np.abs(w)).sum(0)), (dz.sum(0), (edz + DEPTH * U * np.abs(dz)).sum(0)))

@@ -4,6 +4,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 import operator_refs as ref
 import oracle
@@ -122,3 +123,46 @@ def test_operators_refuse_a_null_plan_before_any_device_work():
     assert ssa.lib.ssa_rotary(None, a(v), None, None, None, 1e-6, a(r), 96, 1, a(v), None, None) == 1
     assert ssa.lib.ssa_rotary_backward(None, a(v), None, None, None, None, None, 1e-6, a(r), 96, 1, a(v), None, None,
                                        None, None) == 1
+
+
+# ---- group normalisation -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("act", [None, "silu", "gelu"])
+def test_group_norm_is_torchs_per_sequence(act):
+    rng = np.random.default_rng(1)
+    cu = np.array([0, 5, 5, 6, 20])
+    x, w, b = rng.standard_normal((20, 12)) * 3 + 1, rng.random(12) + 0.5, rng.standard_normal(12)
+    (y, _), (mean, _), (rstd, _) = ref.group_norm(x, cu, 3, w, b, 1e-3, act)
+    f = {None: lambda t: t, "silu": torch.nn.functional.silu, "gelu": torch.nn.functional.gelu}[act]
+    for s, (a, e) in enumerate(zip(cu, cu[1:])):
+        if a == e:
+            assert (mean[s] == 0).all() and (rstd[s] == 0).all()
+            continue
+        t = torch.from_numpy(x[a:e].T[None])
+        want = f(torch.nn.functional.group_norm(t, 3, torch.from_numpy(w), torch.from_numpy(b), 1e-3))[0].T.numpy()
+        np.testing.assert_allclose(y[a:e], want, rtol=0, atol=1e-12)
+
+
+@pytest.mark.parametrize("act", [None, "silu", "gelu"])
+@pytest.mark.parametrize("affine", [False, True])
+def test_group_norm_gradient_against_differences(act, affine):
+    rng = np.random.default_rng(2)
+    cu = np.array([0, 7, 7, 8, 19])
+    x, dy = rng.standard_normal((19, 8)), rng.standard_normal((19, 8))
+    w, b = (rng.random(8) + 0.5, rng.standard_normal(8)) if affine else (np.ones(8), np.zeros(8))
+    _, (mean, _), (rstd, _) = ref.group_norm(x, cu, 2, w, b, 1e-2, act)
+    grads = ref.group_norm_grad(dy, x, mean, rstd, cu, 2, *((w, b) if affine else (None, None)), act)
+    f = lambda *a: float((ref.group_norm(a[0], cu, 2, a[1], a[2], 1e-2, act)[0][0] * dy).sum())  # noqa: E731
+    h = 1e-5
+    for i, v in enumerate((x, w, b)):
+        for _ in range(4):
+            d = rng.standard_normal(v.shape)
+            at = lambda s: f(*[u + s * d if j == i else u for j, u in enumerate((x, w, b))])  # noqa: E731
+            num = (at(h) - at(-h)) / (2 * h)
+            assert abs(num - (grads[i][0] * d).sum()) <= 1e-6 * np.abs(grads[i][0] * d).sum() + 1e-7
+
+
+def test_group_norm_refuses_a_null_plan_before_any_device_work():
+    v, a = ssa._Rows(16, 8), ctypes.addressof
+    assert ssa.lib.ssa_group_norm(None, a(v), 8, 2, None, None, 1e-5, 0, 0, a(v), None, None, None) == 1
+    assert ssa.lib.ssa_group_norm_backward(None, a(v), a(v), 16, 16, 8, 2, None, None, 0, 0, a(v), 16, 16, None) == 1
