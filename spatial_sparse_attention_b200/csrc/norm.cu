@@ -7,10 +7,13 @@
 //   dx = rstd * (dz * gamma - S1 - xhat * S2),  S1 = sum(dz * gamma) / m,  S2 = sum(dz * gamma * xhat) / m
 // over the sequence and group.
 //
-// Bound: HBM. Three launches: sums per channel of every tile of tokens, their merge to groups, and the pass
-// that writes. A thread keeps one vector of channels and walks rows, so channel constants stay in registers
-// whatever the groups' width. A tile that crosses sequences is cut at their borders: part t of
-// the tokens' tiles that lies in sequence s is slot t + s, unique and increasing along the tokens.
+// Bound: HBM. Two launches: sums of every tile of tokens, and the pass that writes, whose CTAs first add up the
+// tiles' sums of their own groups (a few KB from L2, while their first rows arrive). Both cut the rows into column
+// blocks of whole vectors, whatever the groups' width: a thread keeps one vector of channels and walks rows, so
+// channel constants stay in registers; a group across column blocks has sums in each. The second pass takes the
+// tiles in reverse: what the first read last is still in L2.
+// A tile that crosses sequences is cut at their borders: the part of tile t that lies in sequence s has slot
+// t + s in the tables of sums, unique and increasing along the tokens.
 #include <algorithm>
 #include <cmath>
 
@@ -20,11 +23,15 @@ namespace ssa {
 
 namespace {
 
+constexpr int kThreads = 256;
 constexpr int kMaxChannels = 65536;
-constexpr int kMergeThreads = 256;
-// Rows per thread and tile. The variance of a thread's rows comes from sums about its first row: with n rows
-// the cancellation is at most a factor n, as the pivot is one of them; 64 keeps it under 2^-18.
-constexpr int kMaxRowsPerThread = 64;
+// Rows per thread of a full tile. The variance of a thread's rows comes from sums about its first row: with n rows
+// the cancellation is at most a factor n, as the pivot is one of them (sq <= n D^2, D the largest deviation from it, and
+// the squared deviations from the mean are at least D^2 / 2).
+constexpr int kRowsPerThread = 32;
+constexpr int kBlockBytes = 128;        // least width of a column block
+constexpr int kStages = 8;              // rows per thread in flight or in use: forward, gradient
+constexpr int kGradStages = 6;
 
 struct NormArgs {
     const void* x;
@@ -33,19 +40,49 @@ struct NormArgs {
     int64_t x_ts, dy_ts, o_ts;
     const float* gamma;     // null: ones
     const float* beta;      // null: zeros
-    float* mean;            // [B, G]
+    float* mean;            // [B, G] (forward: null when not wanted)
     float* rstd;
-    float2* part;           // [slots][C]: (mean, sum of squared deviations); gradient: (sum dz, sum dz xhat)
-    float2* chan;           // gradient: [B][C] sums per sequence
-    float2* s12;            // gradient: [B][G] (S1, S2)
+    float2* group_part;     // [slots][over][G]: (mean, squared deviations); gradient: sums of gamma dz, gamma dz xhat
+    float2* chan_part;      // gradient: [slots][C] sums of dz, dz xhat
     float* dgamma;
     float* dbeta;
     const SeqInfo* seqs;
-    int64_t N, R;           // tokens; tokens per tile
+    int64_t N;
+    uint32_t R, tiles;      // tokens per tile; tiles
     int32_t B, C, G, width;
+    uint32_t magic;         // ceil(2^32 / width), see group_of
     int32_t nvt, nv, rl;    // vectors per row; vectors and row lanes of a CTA
+    int32_t blocks, over;   // column blocks; blocks that a group can touch
+    int32_t glanes;         // lanes that add a group's channels (power of two)
     float eps;
 };
+
+// c / width for 0 <= c < 65536: c * magic is off by less than c * width < 2^32, under the next quotient's step.
+__device__ __forceinline__ int group_of(const NormArgs& a, int c) {
+    return a.width == 1 ? c : (int)__umulhi((uint32_t)c, a.magic);
+}
+
+// A CTA's column block: vectors [v0, v0 + nvec), channels [c0, c1), groups [g0, g1]; this thread's vector and row lane.
+struct Block {
+    int index, v0, nvec, c0, c1, g0, g1, vec, lane;
+    __device__ __forceinline__ Block(const NormArgs& a, int b, int V) {
+        index = b;
+        v0 = b * a.nv;
+        nvec = min(a.nv, a.nvt - v0);
+        c0 = v0 * V;
+        c1 = c0 + nvec * V;
+        g0 = group_of(a, c0);
+        g1 = group_of(a, c1 - 1);
+        lane = threadIdx.x / a.nv;
+        vec = threadIdx.x - lane * a.nv;
+    }
+    __device__ __forceinline__ bool active(const NormArgs& a) const { return lane < a.rl && vec < nvec; }
+    __device__ __forceinline__ int channel(int V) const { return c0 + vec * V; }
+};
+
+// First column block of a group.
+__device__ __forceinline__ int first_block(const NormArgs& a, int g, int V) { return g * a.width / (a.nv * V); }
+__device__ __forceinline__ int last_block(const NormArgs& a, int g, int V) { return ((g + 1) * a.width - 1) / (a.nv * V); }
 
 // Calls f(s, first token, end) for every part of the tile that lies in one sequence.
 template <typename F>
@@ -60,16 +97,144 @@ __device__ __forceinline__ void for_segments(const NormArgs& a, int64_t tile, F 
     }
 }
 
-// sigma(z). The 16-bit types take the fast exponential (2^-21 relative for |z| < 16); fp32 the exact one.
+// This thread's `count` rows of K arrays, `step` elements apart, its loads STAGES - 1 rows ahead in its own places of
+// the ring: no barrier and no registers for what is in flight. Rows of 2-byte loads, which the
+// asynchronous copy does not take, come in batches through registers instead.
+template <typename T, int V, int K, int STAGES>
+struct Rows {
+    using W = Vec<T, V>;
+    using C = typename W::C;
+    static constexpr bool kRing = sizeof(C) >= 4;
+    static constexpr size_t kBytes = kRing ? STAGES * K * kThreads * sizeof(C) : 0;
+    const T* at[K];
+    int64_t step[K];
+    int count, left;    // rows; those not asked for yet
+    char* ring;
+
+    __device__ __forceinline__ C* place(int stage, int k) const { return (C*)ring + (stage * K + k) * kThreads + threadIdx.x; }
+    __device__ __forceinline__ void fetch(int stage) {
+        if (left > 0) {
+            --left;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                cp_async<sizeof(C)>(place(stage, k), at[k]);
+                at[k] += step[k];
+            }
+        }
+        cp_commit();
+    }
+    // sends off the first rows
+    __device__ __forceinline__ void start() {
+        left = count;
+        if constexpr (kRing) {
+#pragma unroll
+            for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+        }
+    }
+    // row 0, which stays to be read (count > 0)
+    __device__ __forceinline__ void peek(float (&e)[V]) {
+        if constexpr (kRing) {
+            cp_wait<STAGES - 2>();
+            W::unpack(*place(0, 0), e);
+        } else {
+            W::unpack(*reinterpret_cast<const C*>(at[0]), e);
+        }
+    }
+    // f(e) for every row, e[k] being its vector of array k; f may write over the row (in place)
+    template <typename F>
+    __device__ __forceinline__ void each(F f) {
+        if constexpr (kRing) {
+            for (int i = 0; i < count; i += STAGES) {
+#pragma unroll
+                for (int j = 0; j < STAGES; ++j) {
+                    if (i + j < count) {
+                        fetch((j + STAGES - 1) % STAGES);
+                        cp_wait<STAGES - 1>();
+                        float e[K][V];
+#pragma unroll
+                        for (int k = 0; k < K; ++k) W::unpack(*place(j, k), e[k]);
+                        f(e);
+                    }
+                }
+            }
+        } else {
+            constexpr int U = 8;
+            for (int i = 0; i < count; i += U) {
+                C raw[U][K];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (i + u < count) {
+#pragma unroll
+                        for (int k = 0; k < K; ++k) {
+                            raw[u][k] = *reinterpret_cast<const C*>(at[k]);
+                            at[k] += step[k];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (i + u < count) {
+                        float e[K][V];
+#pragma unroll
+                        for (int k = 0; k < K; ++k) W::unpack(raw[u][k], e[k]);
+                        f(e);
+                    }
+                }
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ int row_count(const NormArgs& a, const Block& b, int n) {
+    return b.active(a) && b.lane < n ? (n - b.lane + a.rl - 1) / a.rl : 0;
+}
+
+// Bytes of the channels' sums of a CTA's row lanes (a multiple of 16).
+__host__ __device__ inline size_t red_bytes(const NormArgs& a, int V) { return (sizeof(float2) * a.rl * a.nv * V + 15) / 16 * 16; }
+
+// Adds v over the `lanes` (a power of two) neighbouring lanes; every one gets it.
+template <typename F>
+__device__ __forceinline__ F lane_sum(F v, int lanes) {
+    for (int h = lanes / 2; h > 0; h >>= 1) v += __shfl_xor_sync(0xffffffffu, v, h);
+    return v;
+}
+
+// f(group, channel range relative to c0, lane of the group, lanes) for the block's groups; all threads take part.
+template <typename F>
+__device__ __forceinline__ void for_groups(const NormArgs& a, const Block& b, F f) {
+    const int L = a.glanes;
+    for (int base = b.g0; base <= b.g1; base += kThreads / L) {
+        const int g = base + threadIdx.x / L;
+        const int lo = max(g * a.width, b.c0), hi = g <= b.g1 ? min((g + 1) * a.width, b.c1) : lo;
+        f(g, lo - b.c0, hi - b.c0, threadIdx.x % L, L);
+    }
+}
+
+// ---- activations -------------------------------------------------------------------------------
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// sigma(z). The 16-bit types take the hardware's exponential and reciprocal (2^-20 relative for |z| < 16, far
+// below their rounding); fp32 the exact functions.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float z) {
-    return __fdividef(1.0f, 1.0f + __expf(-z));
+    return rcp(1.0f + ex2(z * -1.4426950408889634f));
 }
 template <>
 __device__ __forceinline__ float sigmoid<float>(float z) {
     return 1.0f / (1.0f + expf(-z));
 }
 
+// z -> act(z)
 template <typename T, int ACT>
 __device__ __forceinline__ float activate(float z) {
     if (ACT == SSA_ACT_SILU) return z * sigmoid<T>(z);
@@ -87,117 +252,190 @@ __device__ __forceinline__ float activate_grad(float z) {
     return 1.0f;
 }
 
-// Per-channel (mean, sum of squared deviations) of every segment of a tile.
+// ---- forward -----------------------------------------------------------------------------------
+
+// Sums of the tile's segments: per group of the column block, mean and squared deviations.
 template <typename T, int V>
-__global__ void k_norm_stats(const __grid_constant__ NormArgs a) {
-    using W = Vec<T, V>;
-    extern __shared__ float2 red[];     // [rl][nv * V]
-    const int vec = threadIdx.x % a.nv, lane = threadIdx.x / a.nv;
-    const int v0 = blockIdx.y * a.nv, row_c = a.nv * V;
-    const bool active = lane < a.rl && v0 + vec < a.nvt;
-    for_segments(a, blockIdx.x, [&](int s, int64_t t, int64_t e) {
-        const int n = (int)(e - t), rl = a.rl;
-        if (active && lane < n) {
-            const T* row = (const T*)a.x + (t + lane) * a.x_ts + (v0 + vec) * V;
-            float p[V], sum[V], sq[V];
-            W::unpack(*reinterpret_cast<const typename W::C*>(row), p);
+__global__ void __launch_bounds__(kThreads) k_norm_stats(const __grid_constant__ NormArgs a) {
+    extern __shared__ __align__(16) char smem[];
+    float2* red = (float2*)smem;        // [rl][nv * V], then the ring
+    const uint32_t tile = blockIdx.x / a.blocks;
+    const Block b(a, blockIdx.x - tile * a.blocks, V);
+    if (tile == 0 && a.mean) {      // sequences without tokens have no tile
+        for (int s = threadIdx.x; s < a.B; s += kThreads)
+            if (a.seqs[s].hi == a.seqs[s].lo)
+                for (int g = b.g0; g <= b.g1; ++g) a.mean[(int64_t)s * a.G + g] = a.rstd[(int64_t)s * a.G + g] = 0.0f;
+    }
+    for_segments(a, tile, [&](int s, int64_t t, int64_t e) {
+        const int n = (int)(e - t), row_c = a.nv * V;
+        Rows<T, V, 1, kStages> rows = {{(const T*)a.x + (t + b.lane) * a.x_ts + b.channel(V)}, {a.rl * a.x_ts},
+                                       row_count(a, b, n), 0, smem + red_bytes(a, V)};
+        rows.start();
+        const int count = rows.count;
+        if (count) {
+            float p[V], sum[V], sq[V];      // p: the first row, negated
+            rows.peek(p);
 #pragma unroll
-            for (int j = 0; j < V; ++j) sum[j] = sq[j] = 0.0f;
-            int k = 0;
-#pragma unroll 4
-            for (int r = lane; r < n; r += rl, ++k) {
-                float v[V];
-                W::unpack(*reinterpret_cast<const typename W::C*>(row + (int64_t)(r - lane) * a.x_ts), v);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float d = v[j] - p[j];
-                    sum[j] += d;
-                    sq[j] = fmaf(d, d, sq[j]);
-                }
+            for (int j = 0; j < V; ++j) {
+                p[j] = -p[j];
+                sum[j] = sq[j] = 0.0f;
             }
-            const float inv = 1.0f / (float)k;
+            rows.each([&](const float (&e)[1][V]) {
+                if constexpr (V > 1) {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                red[lane * row_c + vec * V + j] = make_float2(fmaf(sum[j], inv, p[j]), sq[j] - sum[j] * sum[j] * inv);
+                    for (int j = 0; j < V; j += 2) {
+                        float d0, d1;
+                        add2(d0, d1, e[0][j], e[0][j + 1], p[j], p[j + 1]);
+                        add2(sum[j], sum[j + 1], sum[j], sum[j + 1], d0, d1);
+                        fma2(sq[j], sq[j + 1], d0, d1, d0, d1, sq[j], sq[j + 1]);
+                    }
+                } else {
+                    const float d = e[0][0] + p[0];
+                    sum[0] += d;
+                    sq[0] = fmaf(d, d, sq[0]);
+                }
+            });
+            const float inv = 1.0f / (float)count;
+            float2* mine = red + b.lane * row_c + b.vec * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j) mine[j] = make_float2(fmaf(sum[j], inv, -p[j]), sq[j] - sum[j] * sum[j] * inv);
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < row_c && v0 * V + c < a.C; c += blockDim.x) {
+        // the channels' row lanes into row 0, then the groups' channels
+        const int less = n / a.rl, more = n - less * a.rl, lanes = min(a.rl, n);    // rows per lane; lanes with one more
+        for (int c = threadIdx.x; c < b.c1 - b.c0; c += kThreads) {
             const float first = red[c].x;
             float sum = 0.0f, sq = 0.0f;
-            for (int l = 0; l < rl && l < n; ++l) {
-                const float k = (float)((n - l + rl - 1) / rl), d = red[l * row_c + c].x - first;
+            for (int l = 0; l < lanes; ++l) {
+                const float2 v = red[l * row_c + c];
+                const float k = l < more ? less + 1.0f : (float)less, d = v.x - first;
                 sum = fmaf(k, d, sum);
-                sq += fmaf(k * d, d, red[l * row_c + c].y);
+                sq += fmaf(k * d, d, v.y);
             }
             const float inv = 1.0f / (float)n;
-            a.part[(blockIdx.x + s) * (int64_t)a.C + v0 * V + c] =
-                make_float2(fmaf(sum, inv, first), sq - sum * sum * inv);
+            red[c] = make_float2(fmaf(sum, inv, first), sq - sum * sum * inv);
         }
         __syncthreads();
+        for_groups(a, b, [&](int g, int lo, int hi, int l, int L) {
+            const float first = lo < hi ? red[lo].x : 0.0f;
+            float sum = 0.0f, sq = 0.0f;
+            for (int c = lo + l; c < hi; c += L) {
+                const float d = red[c].x - first;
+                sum += d;
+                sq += fmaf(n * d, d, red[c].y);
+            }
+            sum = lane_sum(sum, L);
+            sq = lane_sum(sq, L);
+            if (l == 0 && lo < hi) {
+                const float d = sum / (float)(hi - lo);
+                a.group_part[((int64_t)(tile + s) * a.over + b.index - first_block(a, g, V)) * a.G + g] =
+                    make_float2(first + d, sq - n * sum * d);
+            }
+        });
+        __syncthreads();    // red is read
     });
 }
 
-// Sum of two doubles over the CTA, in a fixed order; every thread gets it.
-__device__ __forceinline__ double2 block_sum(double2 v, double2* red) {
-    red[threadIdx.x] = v;
-    __syncthreads();
-    for (int h = kMergeThreads / 2; h > 0; h >>= 1) {
-        if (threadIdx.x < h) {
-            red[threadIdx.x].x += red[threadIdx.x + h].x;
-            red[threadIdx.x].y += red[threadIdx.x + h].y;
-        }
-        __syncthreads();
-    }
-    const double2 r = red[0];
-    __syncthreads();
-    return r;
+// f(g, tile sums' table, first slot, slots, overlaps): one warp per group of the column block in sequence s.
+template <typename F>
+__device__ __forceinline__ void for_group_warps(const NormArgs& a, const Block& b, F f) {
+    for (int g = b.g0 + (threadIdx.x >> 5); g <= b.g1; g += kThreads / 32) f(g);
 }
 
-// mean and rstd of group blockIdx.x of sequence blockIdx.y, in fp64 about the first channel's mean.
-__global__ void __launch_bounds__(kMergeThreads) k_norm_merge(const __grid_constant__ NormArgs a) {
-    __shared__ double2 red[kMergeThreads];
-    const int g = blockIdx.x, s = blockIdx.y;
+// Mean and rstd of the block's groups in sequence s into shared memory, from the tiles' in fp64 about the first
+// tile's mean.
+__device__ __forceinline__ void merge_stats(const NormArgs& a, const Block& b, int s, int V, bool write, float2* stats) {
+    const int lane = threadIdx.x & 31;
     const int64_t lo = a.seqs[s].lo, hi = a.seqs[s].hi;
-    if (hi <= lo) {
-        if (threadIdx.x == 0) a.mean[(int64_t)s * a.G + g] = a.rstd[(int64_t)s * a.G + g] = 0.0f;
-        return;
-    }
-    const int64_t ta = lo / a.R, tb = (hi - 1) / a.R;
-    const int cl = min(a.width, kMergeThreads), sl = kMergeThreads / cl;
-    const int l = threadIdx.x / cl;
-    const float2* part = a.part + (int64_t)s * a.C + g * a.width;
-    const double first = part[ta * a.C].x;
-    double2 acc = make_double2(0.0, 0.0);
-    if (l < sl) {
-        for (int c = threadIdx.x % cl; c < a.width; c += cl) {
-            for (int64_t t = ta + l; t <= tb; t += sl) {
-                const float2 v = part[t * a.C + c];
-                const double k = (double)(min(hi, (t + 1) * a.R) - max(lo, t * a.R)), d = (double)v.x - first;
-                acc.x += k * d;
-                acc.y += (double)v.y + k * d * d;
+    const int ta = (int)((uint32_t)lo / a.R), tiles = (int)((uint32_t)(hi - 1) / a.R) - ta + 1;
+    for_group_warps(a, b, [&](int g) {
+        const int o0 = first_block(a, g, V), overlaps = last_block(a, g, V) - o0 + 1, cols = a.nv * V;
+        const float2* part = a.group_part + (int64_t)(ta + s) * a.over * a.G + g;
+        const double first = part->x;
+        double sum = 0.0, sq = 0.0;
+        for (int o = 0; o < overlaps; ++o) {
+            const int from = (o0 + o) * cols;
+            const int c = min((g + 1) * a.width, from + cols) - max(g * a.width, from);    // its channels in the block
+#pragma unroll 4
+            for (int i = lane; i < tiles; i += 32) {
+                const float2 v = part[((int64_t)i * a.over + o) * a.G];
+                const int64_t t = (int64_t)(ta + i) * a.R;
+                const double k = (double)((int)(min(hi, t + a.R) - max(lo, t)) * c), d = (double)v.x - first;
+                sum += k * d;
+                sq += (double)v.y + k * d * d;
             }
         }
-    }
-    acc = block_sum(acc, red);
-    if (threadIdx.x == 0) {
-        const double m = (double)(hi - lo) * a.width, d = acc.x / m;
-        const double var = fmax(acc.y / m - d * d, 0.0);
-        a.mean[(int64_t)s * a.G + g] = (float)(first + d);
+        sum = lane_sum(sum, 32);
+        sq = lane_sum(sq, 32);
+        const double m = (double)(hi - lo) * a.width, d = sum / m, var = fmax(sq / m - d * d, 0.0);
         // a NaN or an infinity among the values leaves NaN here (fmax drops it)
-        const double r = 1.0 / sqrt(var + (double)a.eps);
-        a.rstd[(int64_t)s * a.G + g] = acc.y == acc.y ? (float)r : (float)acc.y;
-    }
+        const float mean = (float)(first + d), rstd = sq == sq ? (float)(1.0 / sqrt(var + (double)a.eps)) : (float)sq;
+        if (lane == 0) {
+            stats[g - b.g0] = make_float2(mean, rstd);
+            if (write && a.mean && o0 == b.index) {
+                a.mean[(int64_t)s * a.G + g] = mean;
+                a.rstd[(int64_t)s * a.G + g] = rstd;
+            }
+        }
+    });
 }
 
-// A thread's channel constants in one sequence.
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(kThreads, 4) k_norm_apply(const __grid_constant__ NormArgs a) {
+    extern __shared__ __align__(16) char smem[];
+    float2* stats = (float2*)(smem + Rows<T, V, 1, kStages>::kBytes);     // the block's groups, after the ring
+    const uint32_t i = gridDim.x - 1 - blockIdx.x, tile = i / a.blocks;
+    const Block b(a, i - tile * a.blocks, V);
+    for_segments(a, tile, [&](int s, int64_t t, int64_t e) {
+        const int c0 = b.channel(V);
+        Rows<T, V, 1, kStages> rows = {{(const T*)a.x + (t + b.lane) * a.x_ts + c0}, {a.rl * a.x_ts},
+                                       row_count(a, b, (int)(e - t)), 0, smem};
+        rows.start();
+        merge_stats(a, b, s, V, t == a.seqs[s].lo, stats);
+        __syncthreads();
+        if (rows.count) {
+            float mean[V], scale[V], beta[V];       // mean: negated
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float2 st = stats[group_of(a, c0 + j) - b.g0];
+                mean[j] = -st.x;
+                scale[j] = st.y * (a.gamma ? a.gamma[c0 + j] : 1.0f);
+                beta[j] = a.beta ? a.beta[c0 + j] : 0.0f;
+            }
+            const int64_t out_step = a.rl * a.o_ts;
+            T* out = (T*)a.out + (t + b.lane) * a.o_ts + c0;
+            rows.each([&](const float (&e)[1][V]) {
+                float z[V];
+                if constexpr (V > 1) {
+#pragma unroll
+                    for (int j = 0; j < V; j += 2) {
+                        add2(z[j], z[j + 1], e[0][j], e[0][j + 1], mean[j], mean[j + 1]);
+                        fma2(z[j], z[j + 1], z[j], z[j + 1], scale[j], scale[j + 1], beta[j], beta[j + 1]);
+                    }
+                } else {
+                    z[0] = fmaf(e[0][0] + mean[0], scale[0], beta[0]);
+                }
+#pragma unroll
+                for (int j = 0; j < V; ++j) z[j] = activate<T, ACT>(z[j]);
+                __stcs(reinterpret_cast<typename Vec<T, V>::C*>(out), Vec<T, V>::pack(z));
+                out += out_step;
+            });
+        }
+        __syncthreads();    // stats are read
+    });
+}
+
+// ---- gradient ------------------------------------------------------------------------------------
+
+// A thread's channel constants in one sequence (mean negated).
 template <int V>
 struct Channels {
     float mean[V], rstd[V], gamma[V], beta[V];
     __device__ __forceinline__ void load(const NormArgs& a, int s, int c0) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t at = (int64_t)s * a.G + (c0 + j) / a.width;
-            mean[j] = a.mean[at];
+            const int64_t at = (int64_t)s * a.G + group_of(a, c0 + j);
+            mean[j] = -a.mean[at];
             rstd[j] = a.rstd[at];
             gamma[j] = a.gamma ? a.gamma[c0 + j] : 1.0f;
             beta[j] = a.beta ? a.beta[c0 + j] : 0.0f;
@@ -205,230 +443,272 @@ struct Channels {
     }
 };
 
+// xhat and dz of one row's vector: e = {x, dy}.
 template <typename T, int V, int ACT>
-__global__ void k_norm_apply(const __grid_constant__ NormArgs a) {
-    using W = Vec<T, V>;
-    const int vec = blockIdx.y * a.nv + threadIdx.x % a.nv, lane = threadIdx.x / a.nv;
-    if (lane >= a.rl || vec >= a.nvt) return;
-    for_segments(a, blockIdx.x, [&](int s, int64_t t, int64_t e) {
-        Channels<V> ch;
-        ch.load(a, s, vec * V);
-        float scale[V];
+__device__ __forceinline__ void row_grad(const Channels<V>& ch, const float (&e)[2][V], float (&xhat)[V], float (&dz)[V]) {
+    if constexpr (V > 1) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) scale[j] = ch.rstd[j] * ch.gamma[j];
-        const T* x = (const T*)a.x + vec * V;
-        T* out = (T*)a.out + vec * V;
-#pragma unroll 4
-        for (int64_t r = t + lane; r < e; r += a.rl) {
-            float v[V];
-            W::unpack(*reinterpret_cast<const typename W::C*>(x + r * a.x_ts), v);
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = activate<T, ACT>(fmaf(v[j] - ch.mean[j], scale[j], ch.beta[j]));
-            *reinterpret_cast<typename W::C*>(out + r * a.o_ts) = W::pack(v);
+        for (int j = 0; j < V; j += 2) {
+            add2(xhat[j], xhat[j + 1], e[0][j], e[0][j + 1], ch.mean[j], ch.mean[j + 1]);     // mean: negated
+            mul2(xhat[j], xhat[j + 1], xhat[j], xhat[j + 1], ch.rstd[j], ch.rstd[j + 1]);
+            if constexpr (ACT == SSA_ACT_NONE) {
+                dz[j] = e[1][j];
+                dz[j + 1] = e[1][j + 1];
+            } else {
+                float z0, z1;
+                fma2(z0, z1, xhat[j], xhat[j + 1], ch.gamma[j], ch.gamma[j + 1], ch.beta[j], ch.beta[j + 1]);
+                mul2(dz[j], dz[j + 1], e[1][j], e[1][j + 1], activate_grad<T, ACT>(z0), activate_grad<T, ACT>(z1));
+            }
         }
-    });
+    } else {
+        xhat[0] = (e[0][0] + ch.mean[0]) * ch.rstd[0];
+        dz[0] = e[1][0] * activate_grad<T, ACT>(fmaf(xhat[0], ch.gamma[0], ch.beta[0]));
+    }
 }
 
-// Per-channel sums of dz and dz * xhat of every segment of a tile.
+template <typename T, int V>
+__device__ __forceinline__ Rows<T, V, 2, kGradStages> grad_rows(const NormArgs& a, const Block& b, int64_t t, int n, char* ring) {
+    return {{(const T*)a.x + (t + b.lane) * a.x_ts + b.channel(V), (const T*)a.dy + (t + b.lane) * a.dy_ts + b.channel(V)},
+            {a.rl * a.x_ts, a.rl * a.dy_ts}, row_count(a, b, n), 0, ring};
+}
+
+// Sums of the tile's segments: per channel dz and dz * xhat, per group of the column block the same times gamma.
 template <typename T, int V, int ACT>
-__global__ void k_norm_grad_sums(const __grid_constant__ NormArgs a) {
-    using W = Vec<T, V>;
-    extern __shared__ float2 red[];
-    const int vec = threadIdx.x % a.nv, lane = threadIdx.x / a.nv;
-    const int v0 = blockIdx.y * a.nv, row_c = a.nv * V;
-    const bool active = lane < a.rl && v0 + vec < a.nvt;
-    for_segments(a, blockIdx.x, [&](int s, int64_t t, int64_t e) {
-        if (active) {
+__global__ void __launch_bounds__(kThreads, 2) k_norm_grad_sums(const __grid_constant__ NormArgs a) {
+    extern __shared__ __align__(16) char smem[];
+    float2* red = (float2*)smem;
+    const uint32_t tile = blockIdx.x / a.blocks;
+    const Block b(a, blockIdx.x - tile * a.blocks, V);
+    for_segments(a, tile, [&](int s, int64_t t, int64_t e) {
+        const int n = (int)(e - t), row_c = a.nv * V, lanes = min(a.rl, n);
+        auto rows = grad_rows<T, V>(a, b, t, n, smem + red_bytes(a, V));
+        rows.start();
+        if (rows.count) {
             Channels<V> ch;
-            ch.load(a, s, (v0 + vec) * V);
+            ch.load(a, s, b.channel(V));
             float s0[V], s1[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) s0[j] = s1[j] = 0.0f;
-            const T* x = (const T*)a.x + (v0 + vec) * V;
-            const T* dy = (const T*)a.dy + (v0 + vec) * V;
-#pragma unroll 2
-            for (int64_t r = t + lane; r < e; r += a.rl) {
-                float v[V], d[V];
-                W::unpack(*reinterpret_cast<const typename W::C*>(x + r * a.x_ts), v);
-                W::unpack(*reinterpret_cast<const typename W::C*>(dy + r * a.dy_ts), d);
+            rows.each([&](const float (&e)[2][V]) {
+                float xhat[V], dz[V];
+                row_grad<T, V, ACT>(ch, e, xhat, dz);
+                if constexpr (V > 1) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float xhat = (v[j] - ch.mean[j]) * ch.rstd[j];
-                    const float dz = d[j] * activate_grad<T, ACT>(fmaf(xhat, ch.gamma[j], ch.beta[j]));
-                    s0[j] += dz;
-                    s1[j] = fmaf(dz, xhat, s1[j]);
+                    for (int j = 0; j < V; j += 2) {
+                        add2(s0[j], s0[j + 1], s0[j], s0[j + 1], dz[j], dz[j + 1]);
+                        fma2(s1[j], s1[j + 1], dz[j], dz[j + 1], xhat[j], xhat[j + 1], s1[j], s1[j + 1]);
+                    }
+                } else {
+                    s0[0] += dz[0];
+                    s1[0] = fmaf(dz[0], xhat[0], s1[0]);
                 }
-            }
+            });
+            float2* mine = red + b.lane * row_c + b.vec * V;
 #pragma unroll
-            for (int j = 0; j < V; ++j) red[lane * row_c + vec * V + j] = make_float2(s0[j], s1[j]);
+            for (int j = 0; j < V; ++j) mine[j] = make_float2(s0[j], s1[j]);
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < row_c && v0 * V + c < a.C; c += blockDim.x) {
-            float2 sum = make_float2(0.0f, 0.0f);
-            for (int l = 0; l < a.rl; ++l) {
+        for (int c = threadIdx.x; c < b.c1 - b.c0; c += kThreads) {
+            float2 sum = red[c];
+            for (int l = 1; l < lanes; ++l) {
                 sum.x += red[l * row_c + c].x;
                 sum.y += red[l * row_c + c].y;
             }
-            a.part[(blockIdx.x + s) * (int64_t)a.C + v0 * V + c] = sum;
+            a.chan_part[(int64_t)(tile + s) * a.C + b.c0 + c] = sum;
+            const float gamma = a.gamma ? a.gamma[b.c0 + c] : 1.0f;
+            red[c] = make_float2(sum.x * gamma, sum.y * gamma);
         }
+        __syncthreads();
+        for_groups(a, b, [&](int g, int lo, int hi, int l, int L) {
+            float s1 = 0.0f, s2 = 0.0f;
+            for (int c = lo + l; c < hi; c += L) {
+                s1 += red[c].x;
+                s2 += red[c].y;
+            }
+            s1 = lane_sum(s1, L);
+            s2 = lane_sum(s2, L);
+            if (l == 0 && lo < hi)
+                a.group_part[((int64_t)(tile + s) * a.over + b.index - first_block(a, g, V)) * a.G + g] = make_float2(s1, s2);
+        });
         __syncthreads();
     });
 }
 
-// The channels' sums over sequence blockIdx.y, and S1, S2 of group blockIdx.x.
-__global__ void __launch_bounds__(kMergeThreads) k_norm_grad_merge(const __grid_constant__ NormArgs a) {
-    __shared__ double2 red[kMergeThreads];
-    const int g = blockIdx.x, s = blockIdx.y;
+// rstd * (S1, S2), negated, of the block's groups in sequence s into shared memory.
+__device__ __forceinline__ void merge_sums(const NormArgs& a, const Block& b, int s, int V, float2* sums) {
+    const int lane = threadIdx.x & 31;
     const int64_t lo = a.seqs[s].lo, hi = a.seqs[s].hi;
-    const int cl = min(a.width, kMergeThreads), sl = kMergeThreads / cl;
-    const int col = threadIdx.x % cl, l = threadIdx.x / cl;
-    float2* chan = a.chan + (int64_t)s * a.C + g * a.width;
-    if (hi <= lo) {
-        for (int c = threadIdx.x; c < a.width; c += kMergeThreads) chan[c] = make_float2(0.0f, 0.0f);
-        return;
-    }
-    const int64_t ta = lo / a.R, tb = (hi - 1) / a.R;
-    const float2* part = a.part + (int64_t)s * a.C + g * a.width;
-    double2 total = make_double2(0.0, 0.0);
-    for (int c0 = 0; c0 < a.width; c0 += cl) {
-        const int c = c0 + col;
-        double2 acc = make_double2(0.0, 0.0);
-        if (l < sl && c < a.width) {
-            for (int64_t t = ta + l; t <= tb; t += sl) {
-                const float2 v = part[t * a.C + c];
+    const int ta = (int)((uint32_t)lo / a.R), tiles = (int)((uint32_t)(hi - 1) / a.R) - ta + 1;
+    for_group_warps(a, b, [&](int g) {
+        const int overlaps = last_block(a, g, V) - first_block(a, g, V) + 1;
+        const float2* part = a.group_part + (int64_t)(ta + s) * a.over * a.G + g;
+        double s1 = 0.0, s2 = 0.0;
+        for (int o = 0; o < overlaps; ++o) {
+#pragma unroll 4
+            for (int i = lane; i < tiles; i += 32) {
+                const float2 v = part[((int64_t)i * a.over + o) * a.G];
+                s1 += v.x;
+                s2 += v.y;
+            }
+        }
+        s1 = lane_sum(s1, 32);
+        s2 = lane_sum(s2, 32);
+        if (lane == 0) {
+            const double f = -(double)a.rstd[(int64_t)s * a.G + g] / ((double)(hi - lo) * a.width);
+            sums[g - b.g0] = make_float2((float)(f * s1), (float)(f * s2));
+        }
+    });
+}
+
+// The weights' gradients of 32 channels: the sums of all slots, in fp64. Slots that no segment has (a tile without
+// tokens of the sequence) are skipped: slot i belongs to sequence s where i - s is one of its tiles.
+__device__ __forceinline__ void merge_weights(const NormArgs& a, int c0, double2* red) {
+    const int c = c0 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    double2 acc = make_double2(0.0, 0.0);
+    if (c < a.C) {
+        for (int s = 0; s < a.B; ++s) {
+            const int64_t lo = a.seqs[s].lo, hi = a.seqs[s].hi;
+            if (hi <= lo) continue;
+            const int64_t from = (uint32_t)lo / a.R + s, to = (uint32_t)(hi - 1) / a.R + s;
+#pragma unroll 4
+            for (int64_t i = from + w; i <= to; i += kThreads / 32) {
+                const float2 v = a.chan_part[i * a.C + c];
                 acc.x += v.x;
                 acc.y += v.y;
             }
         }
-        red[threadIdx.x] = acc;
-        __syncthreads();
-        if (l == 0 && c < a.width) {
-            for (int i = 1; i < sl; ++i) {
-                acc.x += red[i * cl + col].x;
-                acc.y += red[i * cl + col].y;
-            }
-            chan[c] = make_float2((float)acc.x, (float)acc.y);
-            const double gamma = a.gamma ? (double)a.gamma[g * a.width + c] : 1.0;
-            total.x += gamma * acc.x;
-            total.y += gamma * acc.y;
-        }
-        __syncthreads();
     }
-    total = block_sum(total, red);
-    if (threadIdx.x == 0) {
-        const double m = (double)(hi - lo) * a.width;
-        a.s12[(int64_t)s * a.G + g] = make_float2((float)(total.x / m), (float)(total.y / m));
+    red[threadIdx.x] = acc;
+    __syncthreads();
+    if (w == 0 && c < a.C) {
+        for (int i = 1; i < kThreads / 32; ++i) {
+            acc.x += red[i * 32 + threadIdx.x].x;
+            acc.y += red[i * 32 + threadIdx.x].y;
+        }
+        a.dbeta[c] = (float)acc.x;
+        a.dgamma[c] = (float)acc.y;
     }
 }
 
-// dx; and the weights' gradients, the channels' sums over the sequences, by the first tile's CTAs.
+// dx, the tiles in reverse; the first CTAs add up the weights' gradients, 32 channels each.
 template <typename T, int V, int ACT>
-__global__ void k_norm_grad_apply(const __grid_constant__ NormArgs a) {
-    using W = Vec<T, V>;
-    if (blockIdx.x == 0) {
-        for (int i = threadIdx.x; i < a.nv * V; i += blockDim.x) {
-            const int c = blockIdx.y * a.nv * V + i;
-            if (c >= a.C) break;
-            double b = 0.0, g = 0.0;
-            for (int s = 0; s < a.B; ++s) {
-                const float2 v = a.chan[(int64_t)s * a.C + c];
-                b += v.x;
-                g += v.y;
-            }
-            a.dbeta[c] = (float)b;
-            a.dgamma[c] = (float)g;
-        }
+__global__ void __launch_bounds__(kThreads, 2) k_norm_grad_apply(const __grid_constant__ NormArgs a) {
+    extern __shared__ __align__(16) char smem[];
+    float2* sums = (float2*)(smem + Rows<T, V, 2, kGradStages>::kBytes);
+    const uint32_t weights = (a.C + 31) / 32;
+    if (blockIdx.x < weights) {
+        merge_weights(a, blockIdx.x * 32, (double2*)smem);
+        return;
     }
-    const int vec = blockIdx.y * a.nv + threadIdx.x % a.nv, lane = threadIdx.x / a.nv;
-    if (lane >= a.rl || vec >= a.nvt) return;
-    for_segments(a, blockIdx.x, [&](int s, int64_t t, int64_t e) {
-        Channels<V> ch;
-        ch.load(a, s, vec * V);
-        float S1[V], S2[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float2 v = a.s12[(int64_t)s * a.G + (vec * V + j) / a.width];
-            S1[j] = v.x;
-            S2[j] = v.y;
-        }
-        const T* x = (const T*)a.x + vec * V;
-        const T* dy = (const T*)a.dy + vec * V;
-        T* out = (T*)a.out + vec * V;
-#pragma unroll 2
-        for (int64_t r = t + lane; r < e; r += a.rl) {
-            float v[V], d[V];
-            W::unpack(*reinterpret_cast<const typename W::C*>(x + r * a.x_ts), v);
-            W::unpack(*reinterpret_cast<const typename W::C*>(dy + r * a.dy_ts), d);
+    const uint32_t i = gridDim.x - 1 - blockIdx.x, tile = i / a.blocks;
+    const Block b(a, i - tile * a.blocks, V);
+    for_segments(a, tile, [&](int s, int64_t t, int64_t e) {
+        auto rows = grad_rows<T, V>(a, b, t, (int)(e - t), smem);
+        rows.start();
+        merge_sums(a, b, s, V, sums);
+        __syncthreads();
+        if (rows.count) {
+            const int c0 = b.channel(V);
+            Channels<V> ch;
+            ch.load(a, s, c0);
+            float S1[V], S2[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float xhat = (v[j] - ch.mean[j]) * ch.rstd[j];
-                const float dz = d[j] * activate_grad<T, ACT>(fmaf(xhat, ch.gamma[j], ch.beta[j]));
-                v[j] = ch.rstd[j] * (fmaf(dz, ch.gamma[j], -S1[j]) - xhat * S2[j]);
+                const float2 v = sums[group_of(a, c0 + j) - b.g0];
+                S1[j] = v.x;
+                S2[j] = v.y;
             }
-            *reinterpret_cast<typename W::C*>(out + r * a.o_ts) = W::pack(v);
+            const int64_t out_step = a.rl * a.o_ts;
+            T* out = (T*)a.out + (t + b.lane) * a.o_ts + c0;
+            rows.each([&](const float (&e)[2][V]) {
+                float xhat[V], dz[V];
+                row_grad<T, V, ACT>(ch, e, xhat, dz);
+                if constexpr (V > 1) {
+#pragma unroll
+                    for (int j = 0; j < V; j += 2) {
+                        mul2(dz[j], dz[j + 1], dz[j], dz[j + 1], ch.gamma[j], ch.gamma[j + 1]);
+                        fma2(dz[j], dz[j + 1], dz[j], dz[j + 1], ch.rstd[j], ch.rstd[j + 1], S1[j], S1[j + 1]);
+                        fma2(dz[j], dz[j + 1], xhat[j], xhat[j + 1], S2[j], S2[j + 1], dz[j], dz[j + 1]);
+                    }
+                } else {
+                    dz[0] = fmaf(dz[0] * ch.gamma[0], ch.rstd[0], fmaf(xhat[0], S2[0], S1[0]));
+                }
+                __stcs(reinterpret_cast<typename Vec<T, V>::C*>(out), Vec<T, V>::pack(dz));
+                out += out_step;
+            });
         }
+        __syncthreads();
     });
 }
 
 // ---- host --------------------------------------------------------------------------------------
 
 struct Launch {
-    dim3 grid;
-    int threads;
-    size_t smem;
     bool grad;
-    int act;
+    int act, V;
     cudaStream_t st;
 };
 
 template <typename T, int V, int ACT>
-void launch_act(const NormArgs& a, const Launch& l) {
+bool launch_act(const NormArgs& a, const Launch& l) {
+    const unsigned grid = a.tiles * (unsigned)a.blocks;
+    const size_t red = red_bytes(a, V), groups = sizeof(float2) * std::min(a.G, a.nv * V);    // at most 16 KB each
+    auto go = [&](void (*kernel)(NormArgs), unsigned ctas, size_t smem) {
+        if (!allow_smem((const void*)kernel, smem)) return false;
+        kernel<<<ctas, kThreads, smem, l.st>>>(a);
+        note_launch();
+        return true;
+    };
     if (l.grad) {
-        k_norm_grad_sums<T, V, ACT><<<l.grid, l.threads, l.smem, l.st>>>(a);
-        k_norm_grad_merge<<<dim3(a.G, a.B), kMergeThreads, 0, l.st>>>(a);
-        k_norm_grad_apply<T, V, ACT><<<l.grid, l.threads, 0, l.st>>>(a);
-    } else {
-        k_norm_stats<T, V><<<l.grid, l.threads, l.smem, l.st>>>(a);
-        k_norm_merge<<<dim3(a.G, a.B), kMergeThreads, 0, l.st>>>(a);
-        k_norm_apply<T, V, ACT><<<l.grid, l.threads, 0, l.st>>>(a);
+        const size_t ring = Rows<T, V, 2, kGradStages>::kBytes;
+        return go(k_norm_grad_sums<T, V, ACT>, grid, red + ring) &&
+               go(k_norm_grad_apply<T, V, ACT>, grid + (unsigned)cdiv(a.C, 32), std::max(ring + groups, sizeof(double2) * kThreads));
     }
-    note_launch(3);
+    const size_t ring = Rows<T, V, 1, kStages>::kBytes;
+    return go(k_norm_stats<T, V>, grid, red + ring) && go(k_norm_apply<T, V, ACT>, grid, ring + groups);
 }
 
 template <typename T, int V>
-void launch_vec(const NormArgs& a, const Launch& l) {
-    if (l.act == SSA_ACT_SILU) launch_act<T, V, SSA_ACT_SILU>(a, l);
-    else if (l.act == SSA_ACT_GELU) launch_act<T, V, SSA_ACT_GELU>(a, l);
-    else launch_act<T, V, SSA_ACT_NONE>(a, l);
+bool launch_vec(const NormArgs& a, const Launch& l) {
+    if (l.act == SSA_ACT_SILU) return launch_act<T, V, SSA_ACT_SILU>(a, l);
+    if (l.act == SSA_ACT_GELU) return launch_act<T, V, SSA_ACT_GELU>(a, l);
+    return launch_act<T, V, SSA_ACT_NONE>(a, l);
 }
 
 template <typename T>
-void launch_type(const NormArgs& a, const Launch& l, int V) {
+bool launch_type(const NormArgs& a, const Launch& l) {
     if constexpr (sizeof(T) == 2) {
-        if (V == 8) return launch_vec<T, 8>(a, l);
+        if (l.V == 8) return launch_vec<T, 8>(a, l);
     }
-    if (V == 4) launch_vec<T, 4>(a, l);
-    else if (V == 2) launch_vec<T, 2>(a, l);
-    else launch_vec<T, 1>(a, l);
+    if (l.V == 4) return launch_vec<T, 4>(a, l);
+    if (l.V == 2) return launch_vec<T, 2>(a, l);
+    return launch_vec<T, 1>(a, l);
 }
 
-// Vectors per CTA and row lanes: the split of a row's vectors that keeps most threads of a CTA of up to 288
-// busy, wide CTAs first.
-void shape_cta(int nvt, int* nv, int* rl, int* threads) {
-    double best = 0.0;
-    const int least = (nvt + 287) / 288;
-    for (int n = least; n < least + 64; ++n) {
-        const int w = (nvt + n - 1) / n;
-        if (w < 4 && n > least) break;
-        const int r = std::max(1, 288 / w), th = (w * r + 31) / 32 * 32;
-        const double use = (double)nvt / ((double)((nvt + w - 1) / w) * w) * (w * r) / th;
-        if (use > best + 0.02) {
-            best = use;
-            *nv = w;
-            *rl = r;
-            *threads = th;
+// Column blocks and tiles of a call.
+void shape(NormArgs& a, int V, size_t es, int sms) {
+    a.nvt = a.C / V;
+    // vectors per block: at least kBlockBytes of a row, the narrowest that keeps nine tenths of the threads on vectors
+    const int least = std::min<int>(a.nvt, std::max<int>(1, kBlockBytes / (V * (int)es)));
+    int best = -1;
+    for (int n = least; n <= std::min(a.nvt, std::max(least, 4 * least)) && n <= kThreads; ++n) {
+        const int used = (int)((int64_t)100 * a.nvt * (kThreads / n) / (cdiv(a.nvt, n) * kThreads));
+        if (used > best) {
+            best = used;
+            a.nv = n;
         }
+        if (best >= 90) break;
     }
+    a.rl = kThreads / a.nv;
+    a.blocks = (int32_t)cdiv(a.nvt, a.nv);
+    a.over = std::min<int32_t>(a.blocks, (a.width - 1 + a.nv * V - 1) / (a.nv * V) + 1);
+    a.glanes = 1;
+    while (a.glanes < 32 && a.glanes < std::min(a.width, a.nv * V)) a.glanes *= 2;
+    a.magic = (uint32_t)((((uint64_t)1 << 32) + a.width - 1) / a.width);
+    // tokens per tile, a multiple of the row lanes: kRowsPerThread a thread, less where that leaves SMs without work
+    const int64_t even = cdiv(a.N, std::max<int64_t>(1, 4 * sms / a.blocks));
+    a.R = (uint32_t)(a.rl * std::min<int64_t>(kRowsPerThread, cdiv(even, a.rl)));
+    a.tiles = (uint32_t)cdiv(a.N, a.R);
 }
 
 struct Call {
@@ -485,42 +765,23 @@ ssa_status_t run_norm(Plan* p, const Call& c, int32_t C, int32_t G, float eps, i
     a.G = G;
     a.width = C / G;
     a.eps = eps;
-    a.nvt = C / V;
-    Launch l = {};
-    shape_cta(a.nvt, &a.nv, &a.rl, &l.threads);
-    const int ncol = (int)cdiv(a.nvt, a.nv);
-
     const DeviceScope on(p->device);
     if (!on.ok) return SSA_ERR_CUDA;
-    // tokens per tile: eight CTAs per SM, between 4 and 64 rows a thread
-    const int64_t even = cdiv(N * ncol, 8 * sm_count(p->device));
-    a.R = std::min<int64_t>(std::max<int64_t>(even, 4 * a.rl), (int64_t)kMaxRowsPerThread * a.rl);
-    const int64_t tiles = cdiv(N, a.R), slots = tiles + p->B;
-    l.grid = dim3((unsigned)tiles, (unsigned)ncol);
-    l.smem = sizeof(float2) * a.nv * V * a.rl;
-    l.grad = grad;
-    l.act = act;
-    l.st = st;
-
-    // one buffer: partial sums, and the sequences' sums or the statistics that the caller does not want
-    const int64_t BG = (int64_t)p->B * G, extra = grad ? (int64_t)p->B * C + BG : (c.mean ? 0 : BG);
-    a.part = (float2*)p->alloc(sizeof(float2) * (size_t)(slots * C + extra), st, p->alloc_ctx);
-    if (!a.part) return SSA_ERR_ALLOC;
+    shape(a, V, es, sm_count(p->device));
+    if ((int64_t)a.tiles * a.blocks >= ((int64_t)1 << 30)) return SSA_ERR_UNSUPPORTED;
+    // one buffer of the tiles' sums
+    const int64_t slots = (int64_t)a.tiles + p->B, n_group = slots * a.over * G, n_chan = grad ? slots * C : 0;
+    a.group_part = (float2*)p->alloc(sizeof(float2) * (size_t)(n_group + n_chan), st, p->alloc_ctx);
+    if (!a.group_part) return SSA_ERR_ALLOC;
+    a.chan_part = a.group_part + n_group;
     a.mean = c.mean;
     a.rstd = c.rstd;
-    float2* rest = a.part + slots * C;
-    if (grad) {
-        a.chan = rest;
-        a.s12 = rest + (int64_t)p->B * C;
-    } else if (!c.mean) {
-        a.mean = (float*)rest;
-        a.rstd = a.mean + BG;
-    }
-    if (dt == SSA_F32) launch_type<float>(a, l, V);
-    else if (dt == SSA_BF16) launch_type<__nv_bfloat16>(a, l, V);
-    else launch_type<__half>(a, l, V);
-    p->release(a.part, st, p->alloc_ctx);
-    return cudaGetLastError() == cudaSuccess ? SSA_OK : SSA_ERR_CUDA;
+    const Launch l = {grad, act, V, st};
+    const bool ok = dt == SSA_F32    ? launch_type<float>(a, l)
+                    : dt == SSA_BF16 ? launch_type<__nv_bfloat16>(a, l)
+                                     : launch_type<__half>(a, l);
+    p->release(a.group_part, st, p->alloc_ctx);
+    return ok && cudaGetLastError() == cudaSuccess ? SSA_OK : SSA_ERR_CUDA;
 }
 
 }  // namespace

@@ -568,8 +568,7 @@ int rotary_frequencies(const ssa_rotary_t& r, int32_t D, int32_t* axis, double* 
 
 template <typename A>
 bool launch_one(void (*kernel)(A), const A& a, unsigned grid, size_t smem, cudaStream_t st) {
-    if (smem > 48 * 1024 && cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem))
-        return false;
+    if (!allow_smem((const void*)kernel, smem)) return false;
     kernel<<<grid, kThreads, smem, st>>>(a);
     return true;
 }

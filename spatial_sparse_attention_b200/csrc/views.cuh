@@ -90,6 +90,12 @@ inline int sm_count(int device) {
     return n;
 }
 
+// Lets a kernel take `smem` bytes of dynamic shared memory beside at most 8 KB of its own.
+inline bool allow_smem(const void* kernel, size_t smem) {
+    return smem <= 40 * 1024 ||
+           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+}
+
 // ---- device ------------------------------------------------------------------------------------
 
 template <int BYTES> struct Chunk;
