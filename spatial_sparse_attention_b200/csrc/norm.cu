@@ -28,7 +28,7 @@ constexpr int kMaxChannels = 65536;
 // Rows per thread of a full tile. The variance of a thread's rows comes from sums about its first row: with n rows
 // the cancellation is at most a factor n, as the pivot is one of them (sq <= n D^2, D the largest deviation from it, and
 // the squared deviations from the mean are at least D^2 / 2).
-constexpr int kRowsPerThread = 32;
+constexpr int kRowsPerThread = 48;
 constexpr int kBlockBytes = 128;        // least width of a column block
 constexpr int kStages = 8;              // rows per thread in flight or in use: forward, gradient
 constexpr int kGradStages = 6;
@@ -53,7 +53,7 @@ struct NormArgs {
     uint32_t magic;         // ceil(2^32 / width), see group_of
     int32_t nvt, nv, rl;    // vectors per row; vectors and row lanes of a CTA
     int32_t blocks, over;   // column blocks; blocks that a group can touch
-    int32_t glanes;         // lanes that add a group's channels (power of two)
+    int32_t clanes, glanes; // lanes that add a channel's rows, a group's channels (powers of two)
     float eps;
 };
 
@@ -189,14 +189,27 @@ __device__ __forceinline__ int row_count(const NormArgs& a, const Block& b, int 
     return b.active(a) && b.lane < n ? (n - b.lane + a.rl - 1) / a.rl : 0;
 }
 
-// Bytes of the channels' sums of a CTA's row lanes (a multiple of 16).
-__host__ __device__ inline size_t red_bytes(const NormArgs& a, int V) { return (sizeof(float2) * a.rl * a.nv * V + 15) / 16 * 16; }
+// The channels' sums of a CTA's row lanes: [rl][red_row], rows padded by 64 bytes so that threads which read the
+// same channel of different rows meet in few banks; bytes, a multiple of 16.
+__host__ __device__ inline int red_row(const NormArgs& a, int V) { return a.nv * V + 8; }
+__host__ __device__ inline size_t red_bytes(const NormArgs& a, int V) { return (sizeof(float2) * a.rl * red_row(a, V) + 15) / 16 * 16; }
 
 // Adds v over the `lanes` (a power of two) neighbouring lanes; every one gets it.
 template <typename F>
 __device__ __forceinline__ F lane_sum(F v, int lanes) {
     for (int h = lanes / 2; h > 0; h >>= 1) v += __shfl_xor_sync(0xffffffffu, v, h);
     return v;
+}
+
+// f(channel relative to c0, whether it is one, lane, lanes) for the block's channels, several neighbouring lanes to a
+// channel; all threads take part, those beyond the last channel with channel 0. A channel is done by one warp at once.
+template <typename F>
+__device__ __forceinline__ void for_channels(const NormArgs& a, const Block& b, F f) {
+    const int Q = a.clanes, n = b.c1 - b.c0;
+    for (int base = 0; base < n; base += kThreads / Q) {
+        const int c = base + threadIdx.x / Q;
+        f(c < n ? c : 0, c < n, threadIdx.x % Q, Q);
+    }
 }
 
 // f(group, channel range relative to c0, lane of the group, lanes) for the block's groups; all threads take part.
@@ -252,13 +265,33 @@ __device__ __forceinline__ float activate_grad(float z) {
     return 1.0f;
 }
 
+// z -> act'(z) of two values.
+template <typename T, int ACT>
+__device__ __forceinline__ void activate_grad2(float& z0, float& z1) {
+    if constexpr (ACT == SSA_ACT_SILU) {
+        const float t0 = sigmoid<T>(z0), t1 = sigmoid<T>(z1);
+        float u0, u1;       // t + z t (1 - t)
+        fma2(u0, u1, -t0, -t1, t0, t1, t0, t1);
+        fma2(z0, z1, z0, z1, u0, u1, t0, t1);
+    } else {
+        z0 = activate_grad<T, ACT>(z0);
+        z1 = activate_grad<T, ACT>(z1);
+    }
+}
+
+// The second launch of a call starts while the first one's last CTAs run, sends off its rows and waits here for the
+// first to end.
+__device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- forward -----------------------------------------------------------------------------------
 
 // Sums of the tile's segments: per group of the column block, mean and squared deviations.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) k_norm_stats(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(16) char smem[];
-    float2* red = (float2*)smem;        // [rl][nv * V], then the ring
+    float2* red = (float2*)smem;        // [rl][red_row], then the ring
+    let_next_launch_start();
     const uint32_t tile = blockIdx.x / a.blocks;
     const Block b(a, blockIdx.x - tile * a.blocks, V);
     if (tile == 0 && a.mean) {      // sequences without tokens have no tile
@@ -267,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_stats(const __grid_constant__
                 for (int g = b.g0; g <= b.g1; ++g) a.mean[(int64_t)s * a.G + g] = a.rstd[(int64_t)s * a.G + g] = 0.0f;
     }
     for_segments(a, tile, [&](int s, int64_t t, int64_t e) {
-        const int n = (int)(e - t), row_c = a.nv * V;
+        const int n = (int)(e - t), row_c = red_row(a, V);
         Rows<T, V, 1, kStages> rows = {{(const T*)a.x + (t + b.lane) * a.x_ts + b.channel(V)}, {a.rl * a.x_ts},
                                        row_count(a, b, n), 0, smem + red_bytes(a, V)};
         rows.start();
@@ -303,18 +336,20 @@ __global__ void __launch_bounds__(kThreads) k_norm_stats(const __grid_constant__
         __syncthreads();
         // the channels' row lanes into row 0, then the groups' channels
         const int less = n / a.rl, more = n - less * a.rl, lanes = min(a.rl, n);    // rows per lane; lanes with one more
-        for (int c = threadIdx.x; c < b.c1 - b.c0; c += kThreads) {
+        for_channels(a, b, [&](int c, bool valid, int q, int Q) {
             const float first = red[c].x;
             float sum = 0.0f, sq = 0.0f;
-            for (int l = 0; l < lanes; ++l) {
+            for (int l = q; l < lanes; l += Q) {
                 const float2 v = red[l * row_c + c];
                 const float k = l < more ? less + 1.0f : (float)less, d = v.x - first;
                 sum = fmaf(k, d, sum);
                 sq += fmaf(k * d, d, v.y);
             }
+            sum = lane_sum(sum, Q);
+            sq = lane_sum(sq, Q);
             const float inv = 1.0f / (float)n;
-            red[c] = make_float2(fmaf(sum, inv, first), sq - sum * sum * inv);
-        }
+            if (q == 0 && valid) red[c] = make_float2(fmaf(sum, inv, first), sq - sum * sum * inv);
+        });
         __syncthreads();
         for_groups(a, b, [&](int g, int lo, int hi, int l, int L) {
             const float first = lo < hi ? red[lo].x : 0.0f;
@@ -391,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_norm_apply(const __grid_constan
         Rows<T, V, 1, kStages> rows = {{(const T*)a.x + (t + b.lane) * a.x_ts + c0}, {a.rl * a.x_ts},
                                        row_count(a, b, (int)(e - t)), 0, smem};
         rows.start();
+        wait_for_last_launch();
         merge_stats(a, b, s, V, t == a.seqs[s].lo, stats);
         __syncthreads();
         if (rows.count) {
@@ -427,42 +463,42 @@ __global__ void __launch_bounds__(kThreads, 4) k_norm_apply(const __grid_constan
 
 // ---- gradient ------------------------------------------------------------------------------------
 
-// A thread's channel constants in one sequence (mean negated).
+// A thread's channel constants in one sequence: mean (negated), rstd * gamma, beta. The loops work on x - mean and
+// leave the factors rstd to the sums.
 template <int V>
 struct Channels {
-    float mean[V], rstd[V], gamma[V], beta[V];
+    float mean[V], scale[V], beta[V];
     __device__ __forceinline__ void load(const NormArgs& a, int s, int c0) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int64_t at = (int64_t)s * a.G + group_of(a, c0 + j);
             mean[j] = -a.mean[at];
-            rstd[j] = a.rstd[at];
-            gamma[j] = a.gamma ? a.gamma[c0 + j] : 1.0f;
+            scale[j] = a.rstd[at] * (a.gamma ? a.gamma[c0 + j] : 1.0f);
             beta[j] = a.beta ? a.beta[c0 + j] : 0.0f;
         }
     }
 };
 
-// xhat and dz of one row's vector: e = {x, dy}.
+// x - mean and dz of one row's vector: e = {x, dy}.
 template <typename T, int V, int ACT>
-__device__ __forceinline__ void row_grad(const Channels<V>& ch, const float (&e)[2][V], float (&xhat)[V], float (&dz)[V]) {
+__device__ __forceinline__ void row_grad(const Channels<V>& ch, const float (&e)[2][V], float (&xc)[V], float (&dz)[V]) {
     if constexpr (V > 1) {
 #pragma unroll
         for (int j = 0; j < V; j += 2) {
-            add2(xhat[j], xhat[j + 1], e[0][j], e[0][j + 1], ch.mean[j], ch.mean[j + 1]);     // mean: negated
-            mul2(xhat[j], xhat[j + 1], xhat[j], xhat[j + 1], ch.rstd[j], ch.rstd[j + 1]);
+            add2(xc[j], xc[j + 1], e[0][j], e[0][j + 1], ch.mean[j], ch.mean[j + 1]);
             if constexpr (ACT == SSA_ACT_NONE) {
                 dz[j] = e[1][j];
                 dz[j + 1] = e[1][j + 1];
             } else {
                 float z0, z1;
-                fma2(z0, z1, xhat[j], xhat[j + 1], ch.gamma[j], ch.gamma[j + 1], ch.beta[j], ch.beta[j + 1]);
-                mul2(dz[j], dz[j + 1], e[1][j], e[1][j + 1], activate_grad<T, ACT>(z0), activate_grad<T, ACT>(z1));
+                fma2(z0, z1, xc[j], xc[j + 1], ch.scale[j], ch.scale[j + 1], ch.beta[j], ch.beta[j + 1]);
+                activate_grad2<T, ACT>(z0, z1);
+                mul2(dz[j], dz[j + 1], e[1][j], e[1][j + 1], z0, z1);
             }
         }
     } else {
-        xhat[0] = (e[0][0] + ch.mean[0]) * ch.rstd[0];
-        dz[0] = e[1][0] * activate_grad<T, ACT>(fmaf(xhat[0], ch.gamma[0], ch.beta[0]));
+        xc[0] = e[0][0] + ch.mean[0];
+        dz[0] = e[1][0] * activate_grad<T, ACT>(fmaf(xc[0], ch.scale[0], ch.beta[0]));
     }
 }
 
@@ -477,10 +513,11 @@ template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kThreads, 2) k_norm_grad_sums(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(16) char smem[];
     float2* red = (float2*)smem;
+    let_next_launch_start();
     const uint32_t tile = blockIdx.x / a.blocks;
     const Block b(a, blockIdx.x - tile * a.blocks, V);
     for_segments(a, tile, [&](int s, int64_t t, int64_t e) {
-        const int n = (int)(e - t), row_c = a.nv * V, lanes = min(a.rl, n);
+        const int n = (int)(e - t), row_c = red_row(a, V), lanes = min(a.rl, n);
         auto rows = grad_rows<T, V>(a, b, t, n, smem + red_bytes(a, V));
         rows.start();
         if (rows.count) {
@@ -490,17 +527,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_grad_sums(const __grid_con
 #pragma unroll
             for (int j = 0; j < V; ++j) s0[j] = s1[j] = 0.0f;
             rows.each([&](const float (&e)[2][V]) {
-                float xhat[V], dz[V];
-                row_grad<T, V, ACT>(ch, e, xhat, dz);
+                float xc[V], dz[V];
+                row_grad<T, V, ACT>(ch, e, xc, dz);
                 if constexpr (V > 1) {
 #pragma unroll
                     for (int j = 0; j < V; j += 2) {
                         add2(s0[j], s0[j + 1], s0[j], s0[j + 1], dz[j], dz[j + 1]);
-                        fma2(s1[j], s1[j + 1], dz[j], dz[j + 1], xhat[j], xhat[j + 1], s1[j], s1[j + 1]);
+                        fma2(s1[j], s1[j + 1], dz[j], dz[j + 1], xc[j], xc[j + 1], s1[j], s1[j + 1]);
                     }
                 } else {
                     s0[0] += dz[0];
-                    s1[0] = fmaf(dz[0], xhat[0], s1[0]);
+                    s1[0] = fmaf(dz[0], xc[0], s1[0]);
                 }
             });
             float2* mine = red + b.lane * row_c + b.vec * V;
@@ -508,16 +545,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_grad_sums(const __grid_con
             for (int j = 0; j < V; ++j) mine[j] = make_float2(s0[j], s1[j]);
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < b.c1 - b.c0; c += kThreads) {
-            float2 sum = red[c];
-            for (int l = 1; l < lanes; ++l) {
-                sum.x += red[l * row_c + c].x;
-                sum.y += red[l * row_c + c].y;
+        for_channels(a, b, [&](int c, bool valid, int q, int Q) {
+            float s0 = 0.0f, s1 = 0.0f;
+            for (int l = q; l < lanes; l += Q) {
+                const float2 v = red[l * row_c + c];
+                s0 += v.x;
+                s1 += v.y;
             }
-            a.chan_part[(int64_t)(tile + s) * a.C + b.c0 + c] = sum;
-            const float gamma = a.gamma ? a.gamma[b.c0 + c] : 1.0f;
-            red[c] = make_float2(sum.x * gamma, sum.y * gamma);
-        }
+            s0 = lane_sum(s0, Q);
+            s1 = lane_sum(s1, Q);
+            if (q == 0 && valid) {
+                s1 *= a.rstd[(int64_t)s * a.G + group_of(a, b.c0 + c)];
+                a.chan_part[(int64_t)(tile + s) * a.C + b.c0 + c] = make_float2(s0, s1);
+                const float gamma = a.gamma ? a.gamma[b.c0 + c] : 1.0f;
+                red[c] = make_float2(s0 * gamma, s1 * gamma);
+            }
+        });
         __syncthreads();
         for_groups(a, b, [&](int g, int lo, int hi, int l, int L) {
             float s1 = 0.0f, s2 = 0.0f;
@@ -534,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_grad_sums(const __grid_con
     });
 }
 
-// rstd * (S1, S2), negated, of the block's groups in sequence s into shared memory.
+// rstd * S1 and rstd^2 * S2, negated, of the block's groups in sequence s into shared memory.
 __device__ __forceinline__ void merge_sums(const NormArgs& a, const Block& b, int s, int V, float2* sums) {
     const int lane = threadIdx.x & 31;
     const int64_t lo = a.seqs[s].lo, hi = a.seqs[s].hi;
@@ -554,8 +597,8 @@ __device__ __forceinline__ void merge_sums(const NormArgs& a, const Block& b, in
         s1 = lane_sum(s1, 32);
         s2 = lane_sum(s2, 32);
         if (lane == 0) {
-            const double f = -(double)a.rstd[(int64_t)s * a.G + g] / ((double)(hi - lo) * a.width);
-            sums[g - b.g0] = make_float2((float)(f * s1), (float)(f * s2));
+            const double r = a.rstd[(int64_t)s * a.G + g], f = -r / ((double)(hi - lo) * a.width);
+            sums[g - b.g0] = make_float2((float)(f * s1), (float)(f * r * s2));
         }
     });
 }
@@ -597,6 +640,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_grad_apply(const __grid_co
     float2* sums = (float2*)(smem + Rows<T, V, 2, kGradStages>::kBytes);
     const uint32_t weights = (a.C + 31) / 32;
     if (blockIdx.x < weights) {
+        wait_for_last_launch();
         merge_weights(a, blockIdx.x * 32, (double2*)smem);
         return;
     }
@@ -605,6 +649,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_grad_apply(const __grid_co
     for_segments(a, tile, [&](int s, int64_t t, int64_t e) {
         auto rows = grad_rows<T, V>(a, b, t, (int)(e - t), smem);
         rows.start();
+        wait_for_last_launch();
         merge_sums(a, b, s, V, sums);
         __syncthreads();
         if (rows.count) {
@@ -621,17 +666,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_grad_apply(const __grid_co
             const int64_t out_step = a.rl * a.o_ts;
             T* out = (T*)a.out + (t + b.lane) * a.o_ts + c0;
             rows.each([&](const float (&e)[2][V]) {
-                float xhat[V], dz[V];
-                row_grad<T, V, ACT>(ch, e, xhat, dz);
+                float xc[V], dz[V];
+                row_grad<T, V, ACT>(ch, e, xc, dz);
                 if constexpr (V > 1) {
 #pragma unroll
                     for (int j = 0; j < V; j += 2) {
-                        mul2(dz[j], dz[j + 1], dz[j], dz[j + 1], ch.gamma[j], ch.gamma[j + 1]);
-                        fma2(dz[j], dz[j + 1], dz[j], dz[j + 1], ch.rstd[j], ch.rstd[j + 1], S1[j], S1[j + 1]);
-                        fma2(dz[j], dz[j + 1], xhat[j], xhat[j + 1], S2[j], S2[j + 1], dz[j], dz[j + 1]);
+                        fma2(dz[j], dz[j + 1], dz[j], dz[j + 1], ch.scale[j], ch.scale[j + 1], S1[j], S1[j + 1]);
+                        fma2(dz[j], dz[j + 1], xc[j], xc[j + 1], S2[j], S2[j + 1], dz[j], dz[j + 1]);
                     }
                 } else {
-                    dz[0] = fmaf(dz[0] * ch.gamma[0], ch.rstd[0], fmaf(xhat[0], S2[0], S1[0]));
+                    dz[0] = fmaf(dz[0], ch.scale[0], fmaf(xc[0], S2[0], S1[0]));
                 }
                 __stcs(reinterpret_cast<typename Vec<T, V>::C*>(out), Vec<T, V>::pack(dz));
                 out += out_step;
@@ -653,19 +697,28 @@ template <typename T, int V, int ACT>
 bool launch_act(const NormArgs& a, const Launch& l) {
     const unsigned grid = a.tiles * (unsigned)a.blocks;
     const size_t red = red_bytes(a, V), groups = sizeof(float2) * std::min(a.G, a.nv * V);    // at most 16 KB each
-    auto go = [&](void (*kernel)(NormArgs), unsigned ctas, size_t smem) {
+    auto go = [&](void (*kernel)(NormArgs), unsigned ctas, size_t smem, bool second) {
         if (!allow_smem((const void*)kernel, smem)) return false;
-        kernel<<<ctas, kThreads, smem, l.st>>>(a);
+        cudaLaunchAttribute early = {};
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t config = {};
+        config.gridDim = dim3(ctas);
+        config.blockDim = dim3(kThreads);
+        config.dynamicSmemBytes = smem;
+        config.stream = l.st;
+        config.attrs = &early;
+        config.numAttrs = second ? 1 : 0;
         note_launch();
-        return true;
+        return cudaLaunchKernelEx(&config, kernel, a) == cudaSuccess;
     };
     if (l.grad) {
         const size_t ring = Rows<T, V, 2, kGradStages>::kBytes;
-        return go(k_norm_grad_sums<T, V, ACT>, grid, red + ring) &&
-               go(k_norm_grad_apply<T, V, ACT>, grid + (unsigned)cdiv(a.C, 32), std::max(ring + groups, sizeof(double2) * kThreads));
+        return go(k_norm_grad_sums<T, V, ACT>, grid, red + ring, false) &&
+               go(k_norm_grad_apply<T, V, ACT>, grid + (unsigned)cdiv(a.C, 32), std::max(ring + groups, sizeof(double2) * kThreads), true);
     }
     const size_t ring = Rows<T, V, 1, kStages>::kBytes;
-    return go(k_norm_stats<T, V>, grid, red + ring) && go(k_norm_apply<T, V, ACT>, grid, ring + groups);
+    return go(k_norm_stats<T, V>, grid, red + ring, false) && go(k_norm_apply<T, V, ACT>, grid, ring + groups, true);
 }
 
 template <typename T, int V>
@@ -686,7 +739,7 @@ bool launch_type(const NormArgs& a, const Launch& l) {
 }
 
 // Column blocks and tiles of a call.
-void shape(NormArgs& a, int V, size_t es, int sms) {
+void shape(NormArgs& a, int V, size_t es, int ctas) {
     a.nvt = a.C / V;
     // vectors per block: at least kBlockBytes of a row, the narrowest that keeps nine tenths of the threads on vectors
     const int least = std::min<int>(a.nvt, std::max<int>(1, kBlockBytes / (V * (int)es)));
@@ -702,11 +755,12 @@ void shape(NormArgs& a, int V, size_t es, int sms) {
     a.rl = kThreads / a.nv;
     a.blocks = (int32_t)cdiv(a.nvt, a.nv);
     a.over = std::min<int32_t>(a.blocks, (a.width - 1 + a.nv * V - 1) / (a.nv * V) + 1);
-    a.glanes = 1;
+    a.clanes = a.glanes = 1;
+    while (a.clanes < 32 && a.clanes * 2 <= a.rl && a.clanes * 2 * a.nv * V <= kThreads) a.clanes *= 2;
     while (a.glanes < 32 && a.glanes < std::min(a.width, a.nv * V)) a.glanes *= 2;
     a.magic = (uint32_t)((((uint64_t)1 << 32) + a.width - 1) / a.width);
-    // tokens per tile, a multiple of the row lanes: kRowsPerThread a thread, less where that leaves SMs without work
-    const int64_t even = cdiv(a.N, std::max<int64_t>(1, 4 * sms / a.blocks));
+    // tokens per tile, a multiple of the row lanes: kRowsPerThread a thread, less where that leaves SMs without CTAs
+    const int64_t even = cdiv(a.N, std::max<int64_t>(1, ctas / a.blocks));
     a.R = (uint32_t)(a.rl * std::min<int64_t>(kRowsPerThread, cdiv(even, a.rl)));
     a.tiles = (uint32_t)cdiv(a.N, a.R);
 }
@@ -767,7 +821,7 @@ ssa_status_t run_norm(Plan* p, const Call& c, int32_t C, int32_t G, float eps, i
     a.eps = eps;
     const DeviceScope on(p->device);
     if (!on.ok) return SSA_ERR_CUDA;
-    shape(a, V, es, sm_count(p->device));
+    shape(a, V, es, (grad ? 2 : 4) * sm_count(p->device));
     if ((int64_t)a.tiles * a.blocks >= ((int64_t)1 << 30)) return SSA_ERR_UNSUPPORTED;
     // one buffer of the tiles' sums
     const int64_t slots = (int64_t)a.tiles + p->B, n_group = slots * a.over * G, n_chan = grad ? slots * C : 0;
