@@ -250,6 +250,10 @@ def _activation(name: Optional[str]) -> int:
     return _ACTIVATION[name]
 
 
+def _like(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _ref(s):
     return None if s is None else ctypes.addressof(s)
 
@@ -275,6 +279,7 @@ class Plan:
         self._h = _vp()
         self.stream = stream
         self.device = coords.device
+        self._f32 = torch.empty(0, dtype=torch.float32, device=coords.device)   # makes fp32 results
         st = _stream(stream)
         if cu_seqlens is None:
             g = (ctypes.c_int32 * 3)(*[int(x) for x in grid])
@@ -449,7 +454,9 @@ class Plan:
         return contextlib.nullcontext() if self.stream is None else torch.cuda.stream(self.stream)
 
     def _stream_of(self) -> int:
-        return (torch.cuda.current_stream(self.device) if self.stream is None else self.stream).cuda_stream
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def rotary(self, q, k=None, rotary: Optional[Rotary] = None, q_gamma=None, k_gamma=None,
                eps: float = 1e-6, q_out=None, k_out=None):
@@ -464,9 +471,9 @@ class Plan:
         gk = None if k is None else _weights(k_gamma, D, q, "k_gamma")
         with self._on_stream():
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                q_out = _like(q)
             if k_out is None and k is not None:
-                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+                k_out = _like(k)
         oq, ok = _heads(q_out, self, q), _heads(k_out, self, q)
         _check(lib.ssa_rotary(self._h, ctypes.addressof(hq), _ref(hk), gq, gk, eps,
                               ctypes.addressof(rotary), D, _DTYPE.get(q.dtype, -1), ctypes.addressof(oq),
@@ -491,12 +498,12 @@ class Plan:
         wq = wk = None
         with self._on_stream():
             if dq is None:
-                dq = torch.empty(dq_out.shape, dtype=dq_out.dtype, device=dq_out.device)
+                dq = _like(dq_out)
             if dk is None and keys:
-                dk = torch.empty(dk_out.shape, dtype=dk_out.dtype, device=dk_out.device)
+                dk = _like(dk_out)
             if norm:
-                wq = torch.empty(D, dtype=torch.float32, device=dq_out.device)
-                wk = torch.empty(D, dtype=torch.float32, device=dq_out.device) if keys else None
+                wq = torch.empty_like(q_gamma)
+                wk = torch.empty_like(k_gamma) if keys and k_gamma is not None else None
         oq, ok = _heads(dq, self, dq_out), _heads(dk, self, dq_out)
         _check(lib.ssa_rotary_backward(self._h, ctypes.addressof(gq_), _ref(gk_), _ref(hq), _ref(hk), gq,
                                        gk, eps, ctypes.addressof(rotary), D, _DTYPE.get(dq_out.dtype, -1),
@@ -519,9 +526,9 @@ class Plan:
         mean = rstd = None
         with self._on_stream():
             if out is None:
-                out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+                out = _like(x)
             if return_stats:
-                mean, rstd = torch.empty(2, self.batch, groups, dtype=torch.float32, device=x.device)
+                mean, rstd = self._f32.new_empty((2, self.batch, groups)).unbind(0)
         vy = _rows(out, self, x)
         _check(lib.ssa_group_norm(self._h, ctypes.addressof(vx), C, groups, wg, wb, eps, act,
                                   _DTYPE.get(x.dtype, -1), ctypes.addressof(vy), _ptr(mean), _ptr(rstd),
@@ -539,8 +546,8 @@ class Plan:
         m, r = _weights(mean, self.batch * groups, x, "mean"), _weights(rstd, self.batch * groups, x, "rstd")
         with self._on_stream():
             if dx is None:
-                dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            dgamma, dbeta = torch.empty(2, C, dtype=torch.float32, device=x.device)
+                dx = _like(x)
+            dgamma, dbeta = self._f32.new_empty((2, C)).unbind(0)
         vo = _rows(dx, self, x)
         _check(lib.ssa_group_norm_backward(self._h, ctypes.addressof(vd), ctypes.addressof(vx), m, r, C, groups,
                                            wg, wb, act, _DTYPE.get(x.dtype, -1), ctypes.addressof(vo),

@@ -16,6 +16,7 @@
 // t + s in the tables of sums, unique and increasing along the tokens.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "views.cuh"
 
@@ -687,9 +688,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_grad_apply(const __grid_co
 
 // ---- host --------------------------------------------------------------------------------------
 
+template <void (*K)(NormArgs)>
+using Kernel = std::integral_constant<void (*)(NormArgs), K>;
+
 struct Launch {
     bool grad;
-    int act, V;
+    int act, V, device;
     cudaStream_t st;
 };
 
@@ -697,8 +701,9 @@ template <typename T, int V, int ACT>
 bool launch_act(const NormArgs& a, const Launch& l) {
     const unsigned grid = a.tiles * (unsigned)a.blocks;
     const size_t red = red_bytes(a, V), groups = sizeof(float2) * std::min(a.G, a.nv * V);    // at most 16 KB each
-    auto go = [&](void (*kernel)(NormArgs), unsigned ctas, size_t smem, bool second) {
-        if (!allow_smem((const void*)kernel, smem)) return false;
+    auto go = [&](auto tag, unsigned ctas, size_t smem, bool second) {
+        constexpr auto kernel = decltype(tag)::value;
+        if (!allow_smem<kernel>(l.device)) return false;
         cudaLaunchAttribute early = {};
         early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         early.val.programmaticStreamSerializationAllowed = 1;
@@ -714,11 +719,11 @@ bool launch_act(const NormArgs& a, const Launch& l) {
     };
     if (l.grad) {
         const size_t ring = Rows<T, V, 2, kGradStages>::kBytes;
-        return go(k_norm_grad_sums<T, V, ACT>, grid, red + ring, false) &&
-               go(k_norm_grad_apply<T, V, ACT>, grid + (unsigned)cdiv(a.C, 32), std::max(ring + groups, sizeof(double2) * kThreads), true);
+        return go(Kernel<k_norm_grad_sums<T, V, ACT>>(), grid, red + ring, false) &&
+               go(Kernel<k_norm_grad_apply<T, V, ACT>>(), grid + (unsigned)cdiv(a.C, 32), std::max(ring + groups, sizeof(double2) * kThreads), true);
     }
     const size_t ring = Rows<T, V, 1, kStages>::kBytes;
-    return go(k_norm_stats<T, V>, grid, red + ring, false) && go(k_norm_apply<T, V, ACT>, grid, ring + groups, true);
+    return go(Kernel<k_norm_stats<T, V>>(), grid, red + ring, false) && go(Kernel<k_norm_apply<T, V, ACT>>(), grid, ring + groups, true);
 }
 
 template <typename T, int V>
@@ -830,7 +835,7 @@ ssa_status_t run_norm(Plan* p, const Call& c, int32_t C, int32_t G, float eps, i
     a.chan_part = a.group_part + n_group;
     a.mean = c.mean;
     a.rstd = c.rstd;
-    const Launch l = {grad, act, V, st};
+    const Launch l = {grad, act, V, p->device, st};
     const bool ok = dt == SSA_F32    ? launch_type<float>(a, l)
                     : dt == SSA_BF16 ? launch_type<__nv_bfloat16>(a, l)
                                      : launch_type<__half>(a, l);

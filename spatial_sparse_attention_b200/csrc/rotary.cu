@@ -48,6 +48,7 @@ struct RotArgs {
     int32_t D, G;                  // head dimension; lanes per row
     int32_t pairs;                 // rotated pairs
     int32_t tile;                  // tokens per tile
+    int32_t device;                // host side
     int32_t ctas0;                 // gradient: CTAs [0, ctas0) work on t[0], the rest on t[1]
     float eps, inv_d, mscale, sgn; // inv_d = 1/D; sgn = -1 turns back
     uint64_t turns[kMaxPairs];
@@ -549,6 +550,11 @@ int rotary_frequencies(const ssa_rotary_t& r, int32_t D, int32_t* axis, double* 
     for (int a = 0; a < 3; ++a) {
         const int w = width[a];
         for (int j = 0; j < w / 2; ++j, ++p) {
+            axis[p] = a;
+            if (a && w == width[a - 1]) {   // the same frequencies as the axis before
+                freq[p] = freq[p - w / 2];
+                continue;
+            }
             double f = std::pow(r.theta, -2.0 * j / w);
             if (r.scaling == SSA_ROTARY_SCALE_LINEAR) {
                 f /= r.scale;
@@ -559,26 +565,25 @@ int rotary_frequencies(const ssa_rotary_t& r, int32_t D, int32_t* axis, double* 
                 g = std::min(1.0, std::max(0.0, g));
                 f *= g + (1.0 - g) / r.scale;
             }
-            axis[p] = a;
             freq[p] = f;
         }
     }
     return p;
 }
 
-template <typename A>
-bool launch_one(void (*kernel)(A), const A& a, unsigned grid, size_t smem, cudaStream_t st) {
-    if (!allow_smem((const void*)kernel, smem)) return false;
-    kernel<<<grid, kThreads, smem, st>>>(a);
+template <void (*KERNEL)(RotArgs)>
+bool launch_one(const RotArgs& a, unsigned grid, size_t smem, cudaStream_t st) {
+    if (!allow_smem<KERNEL>(a.device)) return false;
+    KERNEL<<<grid, kThreads, smem, st>>>(a);
     return true;
 }
 
 template <typename T, int V, bool HALF, int LANES>
 bool launch_lanes(const RotArgs& a, unsigned grid, bool grad, cudaStream_t st) {
     const size_t ring = (size_t)kLane * kThreads, tables = sizeof(float) * 2 * ((size_t)a.tile * tab_stride(a.D) + a.D);
-    if (grad) return launch_one(k_rotary_grad<T, V, HALF, LANES>, a, grid, 2 * kGradStages * ring + tables, st);
-    if (a.t[0].gamma) return launch_one(k_rotary<T, V, HALF, true, LANES>, a, grid, kStages * ring + tables, st);
-    return launch_one(k_rotary<T, V, HALF, false, LANES>, a, grid, kStages * ring + tables, st);
+    if (grad) return launch_one<k_rotary_grad<T, V, HALF, LANES>>(a, grid, 2 * kGradStages * ring + tables, st);
+    if (a.t[0].gamma) return launch_one<k_rotary<T, V, HALF, true, LANES>>(a, grid, kStages * ring + tables, st);
+    return launch_one<k_rotary<T, V, HALF, false, LANES>>(a, grid, kStages * ring + tables, st);
 }
 
 // Loads of 16 and 8 bytes with the lanes per row known at compile time (a shuffle tree and offsets without
@@ -688,6 +693,7 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
     a.G = D * (int)es / 32;
     a.eps = eps;
     a.inv_d = 1.0f / (float)D;
+    a.device = p->device;
     a.mscale = rot->mscale;
     a.sgn = backward ? -1.0f : 1.0f;
 

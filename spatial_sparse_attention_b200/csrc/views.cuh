@@ -90,10 +90,16 @@ inline int sm_count(int device) {
     return n;
 }
 
-// Lets a kernel take `smem` bytes of dynamic shared memory beside at most 8 KB of its own.
-inline bool allow_smem(const void* kernel, size_t smem) {
-    return smem <= 40 * 1024 ||
-           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+// Lets a kernel take any dynamic shared memory that an SM has beside 8 KB of its own; asked for once per kernel and device.
+template <auto KERNEL>
+bool allow_smem(int device) {
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = device >= 0 && device < 64 ? (uint64_t)1 << device : 0;
+    if (bit && (done.load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute((const void*)KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (227 - 8) * 1024) != cudaSuccess)
+        return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
 }
 
 // ---- device ------------------------------------------------------------------------------------
