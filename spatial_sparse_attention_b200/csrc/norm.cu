@@ -9,11 +9,14 @@
 //
 // Bound: HBM. Two launches: sums of every tile of tokens, and the pass that writes, whose CTAs first add up the
 // tiles' sums of their own groups (a few KB from L2, while their first rows arrive). Both cut the rows into column
-// blocks of whole vectors, whatever the groups' width: a thread keeps one vector of channels and walks rows, so
-// channel constants stay in registers; a group across column blocks has sums in each. The second pass takes the
-// tiles in reverse: what the first read last is still in L2.
-// A tile that crosses sequences is cut at their borders: the part of tile t that lies in sequence s has slot
-// t + s in the tables of sums, unique and increasing along the tokens.
+// blocks of 16-byte vectors, whatever the groups' width: a thread keeps one vector of channels and walks rows, so
+// channel constants stay in registers; a group across column blocks has sums in each. Rows that are not aligned
+// to 16 bytes are read in chunks of A elements. The second pass takes the tiles in reverse: what the
+// first read last is still in L2. (Tried and slower: column blocks or units of groups small enough to stay in L2
+// between the passes, as one launch with tickets or as many launches, 913 us and more against 691 for 340,000 tokens x 2112
+// fp16: pieces of rows, 128 to 528 bytes 4 KB apart, cost more than the third pass over memory.)
+// Tile `t` of sequence s holds its tokens [t * R, ...) and has slot lo / R + s + t in the tables of sums: a sequence of n
+// tokens owns hi / R - lo / R + 1 >= ceil(n / R) slots; the tiles beyond its end are empty.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -25,12 +28,14 @@ namespace ssa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kVecBytes = 16;
 constexpr int kMaxChannels = 65536;
 // Rows per thread of a full tile. The variance of a thread's rows comes from sums about its first row: with n rows
 // the cancellation is at most a factor n, as the pivot is one of them (sq <= n D^2, D the largest deviation from it, and
 // the squared deviations from the mean are at least D^2 / 2).
 constexpr int kRowsPerThread = 48;
-constexpr int kBlockBytes = 128;        // least width of a column block
+constexpr int kMaxTiles = 148;
+constexpr int kBlockBytes = 128;        // of a row that a column block's threads read together, at least
 constexpr int kStages = 8;              // rows per thread in flight or in use: forward, gradient
 constexpr int kGradStages = 6;
 
@@ -49,10 +54,10 @@ struct NormArgs {
     float* dbeta;
     const SeqInfo* seqs;
     int64_t N;
-    uint32_t R, tiles;      // tokens per tile; tiles
+    uint32_t R, slots;      // tokens per tile; slots of all sequences
     int32_t B, C, G, width;
     uint32_t magic;         // ceil(2^32 / width), see group_of
-    int32_t nvt, nv, rl;    // vectors per row; vectors and row lanes of a CTA
+    int32_t nvt, nv, rl;    // vectors per row (the last may be partly filled); vectors and row lanes of a CTA
     int32_t blocks, over;   // column blocks; blocks that a group can touch
     int32_t clanes, glanes; // lanes that add a channel's rows, a group's channels (powers of two)
     float eps;
@@ -71,54 +76,104 @@ struct Block {
         v0 = b * a.nv;
         nvec = min(a.nv, a.nvt - v0);
         c0 = v0 * V;
-        c1 = c0 + nvec * V;
+        c1 = min(a.C, c0 + nvec * V);
         g0 = group_of(a, c0);
         g1 = group_of(a, c1 - 1);
         lane = threadIdx.x / a.nv;
         vec = threadIdx.x - lane * a.nv;
     }
     __device__ __forceinline__ bool active(const NormArgs& a) const { return lane < a.rl && vec < nvec; }
-    __device__ __forceinline__ int channel(int V) const { return c0 + vec * V; }
+    // Channel of element j of the thread's vector, relative to c0. Chunks of A elements go round the block's vectors:
+    // what neighbouring threads read or write together is contiguous, whatever A.
+    template <int A>
+    __device__ __forceinline__ int relative(int j) const { return ((j / A) * nvec + vec) * A + j % A; }
+    // the same, inside the block: elements beyond the row take the last channel's constants, nothing is made of them
+    template <int A>
+    __device__ __forceinline__ int channel(int j) const { return min(c0 + relative<A>(j), c1 - 1); }
+    // chunks of the vector that lie in the row
+    template <int A>
+    __device__ __forceinline__ int chunks() const { return (c1 - c0 - vec * A + nvec * A - 1) / (nvec * A); }
 };
 
 // First column block of a group.
 __device__ __forceinline__ int first_block(const NormArgs& a, int g, int V) { return g * a.width / (a.nv * V); }
 __device__ __forceinline__ int last_block(const NormArgs& a, int g, int V) { return ((g + 1) * a.width - 1) / (a.nv * V); }
 
-// Calls f(s, first token, end) for every part of the tile that lies in one sequence.
-template <typename F>
-__device__ __forceinline__ void for_segments(const NormArgs& a, int64_t tile, F f) {
-    int64_t t = tile * a.R;
-    const int64_t end = min(a.N, t + a.R);
-    for (int s = find_seq(a.seqs, a.B, t); t < end; ++s) {
-        const int64_t e = min(a.seqs[s].hi, end);
-        if (e <= t) continue;
-        f(s, t, e);
-        t = e;
+__device__ __forceinline__ uint32_t first_slot(const NormArgs& a, int s) { return (uint32_t)a.seqs[s].lo / a.R + s; }
+
+// The tile of a slot: n tokens of sequence s from t0; tiles: of the sequence.
+struct Tile {
+    int s, n, tiles;
+    int64_t t0;
+    uint32_t slot;
+    bool opens;     // the sequence's first
+    __device__ __forceinline__ Tile(const NormArgs& a, uint32_t i) {
+        int last = a.B - 1;
+        s = 0;
+        while (s < last) {
+            const int mid = (s + last + 1) >> 1;
+            if (first_slot(a, mid) <= i) s = mid; else last = mid - 1;
+        }
+        const int64_t lo = a.seqs[s].lo, hi = a.seqs[s].hi;
+        const uint32_t t = i - first_slot(a, s);
+        slot = i;
+        opens = t == 0;
+        t0 = lo + (int64_t)t * a.R;
+        n = (int)max((int64_t)0, min((int64_t)a.R, hi - t0));
+        tiles = (int)(((uint32_t)(hi - lo) + a.R - 1) / a.R);
     }
-}
+};
+
+// The vectors of this thread's rows, 16 bytes in chunks of A elements `hop` apart; `chunks` of them are inside the row.
+template <typename T, int A>
+struct Pieces {
+    static constexpr int V = kVecBytes / (int)sizeof(T), N = V / A;
+    using W = Vec<T, A>;
+    using C = typename W::C;
+    static __device__ __forceinline__ void unpack(const C& raw, int i, float (&e)[V]) {
+        float v[A];
+        W::unpack(raw, v);
+#pragma unroll
+        for (int j = 0; j < A; ++j) e[i * A + j] = v[j];
+    }
+    static __device__ __forceinline__ void store(T* at, const float (&e)[V], int chunks, int hop) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float v[A];
+#pragma unroll
+            for (int j = 0; j < A; ++j) v[j] = e[i * A + j];
+            if (N == 1 || i < chunks) __stcs(reinterpret_cast<C*>(at + i * hop), W::pack(v));
+        }
+    }
+};
 
 // This thread's `count` rows of K arrays, `step` elements apart, its loads STAGES - 1 rows ahead in its own places of
-// the ring: no barrier and no registers for what is in flight. Rows of 2-byte loads, which the
+// the ring: no barrier and no registers for what is in flight. Rows of 2-byte chunks, which the
 // asynchronous copy does not take, come in batches through registers instead.
-template <typename T, int V, int K, int STAGES>
+template <typename T, int A, int K, int STAGES>
 struct Rows {
-    using W = Vec<T, V>;
-    using C = typename W::C;
+    using P = Pieces<T, A>;
+    using C = typename P::C;
+    static constexpr int V = P::V, N = P::N;
     static constexpr bool kRing = sizeof(C) >= 4;
-    static constexpr size_t kBytes = kRing ? STAGES * K * kThreads * sizeof(C) : 0;
+    static constexpr size_t kBytes = kRing ? STAGES * K * kThreads * kVecBytes : 0;
     const T* at[K];
     int64_t step[K];
-    int count, left;    // rows; those not asked for yet
+    int count, chunks, hop;
     char* ring;
+    int left;           // rows not asked for yet
 
-    __device__ __forceinline__ C* place(int stage, int k) const { return (C*)ring + (stage * K + k) * kThreads + threadIdx.x; }
+    __device__ __forceinline__ C* place(int stage, int k, int i) const {
+        return (C*)ring + ((stage * K + k) * N + i) * kThreads + threadIdx.x;
+    }
     __device__ __forceinline__ void fetch(int stage) {
         if (left > 0) {
             --left;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                cp_async<sizeof(C)>(place(stage, k), at[k]);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (N == 1 || i < chunks) cp_async<sizeof(C)>(place(stage, k, i), at[k] + i * hop);
                 at[k] += step[k];
             }
         }
@@ -132,18 +187,32 @@ struct Rows {
             for (int i = 0; i < STAGES - 1; ++i) fetch(i);
         }
     }
+    // channels beyond the row come out as anything: nothing is made of them
+    __device__ __forceinline__ void read(int stage, int k, float (&e)[V]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) P::unpack(*place(stage, k, i), i, e);
+    }
+    __device__ __forceinline__ void load(const T* from, C (&raw)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (N == 1 || i < chunks) raw[i] = *reinterpret_cast<const C*>(from + i * hop);
+    }
     // row 0, which stays to be read (count > 0)
     __device__ __forceinline__ void peek(float (&e)[V]) {
         if constexpr (kRing) {
             cp_wait<STAGES - 2>();
-            W::unpack(*place(0, 0), e);
+            read(0, 0, e);
         } else {
-            W::unpack(*reinterpret_cast<const C*>(at[0]), e);
+            C raw[N] = {};
+            load(at[0], raw);
+#pragma unroll
+            for (int i = 0; i < N; ++i) P::unpack(raw[i], i, e);
         }
     }
     // f(e) for every row, e[k] being its vector of array k; f may write over the row (in place)
     template <typename F>
     __device__ __forceinline__ void each(F f) {
+        float e[K][V];
         if constexpr (kRing) {
             for (int i = 0; i < count; i += STAGES) {
 #pragma unroll
@@ -151,23 +220,22 @@ struct Rows {
                     if (i + j < count) {
                         fetch((j + STAGES - 1) % STAGES);
                         cp_wait<STAGES - 1>();
-                        float e[K][V];
 #pragma unroll
-                        for (int k = 0; k < K; ++k) W::unpack(*place(j, k), e[k]);
+                        for (int k = 0; k < K; ++k) read(j, k, e[k]);
                         f(e);
                     }
                 }
             }
         } else {
-            constexpr int U = 8;
+            constexpr int U = 4 / K;
             for (int i = 0; i < count; i += U) {
-                C raw[U][K];
+                C raw[U][K][N] = {};
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (i + u < count) {
 #pragma unroll
                         for (int k = 0; k < K; ++k) {
-                            raw[u][k] = *reinterpret_cast<const C*>(at[k]);
+                            load(at[k], raw[u][k]);
                             at[k] += step[k];
                         }
                     }
@@ -175,9 +243,11 @@ struct Rows {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (i + u < count) {
-                        float e[K][V];
 #pragma unroll
-                        for (int k = 0; k < K; ++k) W::unpack(raw[u][k], e[k]);
+                        for (int k = 0; k < K; ++k) {
+#pragma unroll
+                            for (int n = 0; n < N; ++n) P::unpack(raw[u][k][n], n, e[k]);
+                        }
                         f(e);
                     }
                 }
@@ -248,21 +318,56 @@ __device__ __forceinline__ float sigmoid<float>(float z) {
     return 1.0f / (1.0f + expf(-z));
 }
 
+// Phi(-|z|) of the normal distribution, as t p(t) exp(-z^2 / 2) with t = 1 / (1 + 0.3 |z|): p fitted to the scaled complement
+// erfc(x) exp(x^2) / 2 at x = |z| / sqrt(2) <= 10 for least relative error, 3.4e-7 in fp32. For the 16-bit types; `e`
+// is exp(-z^2 / 2), which the gradient needs as well. normcdff, twice as many instructions, bounds the pass that writes
+// in place of memory (570 against 290 us for 135,000 tokens x 1376 bf16); fp32 keeps it.
+__device__ __forceinline__ float normal_tail(float z, float e) {
+    const float t = rcp(fmaf(fabsf(z), 0.3f, 1.0f));
+    float p = fmaf(t, 0.035675015f, -0.157204f);
+    p = fmaf(p, t, 0.20635495f);
+    p = fmaf(p, t, -0.053684855f);
+    p = fmaf(p, t, 0.12856221f);
+    p = fmaf(p, t, 0.09991333f);
+    p = fmaf(p, t, 0.12075398f);
+    p = fmaf(p, t, 0.11962929f);
+    return p * t * e;
+}
+
+// Phi(z) and exp(-z^2 / 2).
+template <typename T>
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+    if constexpr (sizeof(T) == 2) {
+        e = ex2(z * z * -0.72134752f);      // log2(e) / 2
+        const float q = normal_tail(z, e);
+        return z > 0.0f ? 1.0f - q : q;
+    } else {
+        e = expf(-0.5f * z * z);
+        return normcdff(z);
+    }
+}
+
 // z -> act(z)
 template <typename T, int ACT>
 __device__ __forceinline__ float activate(float z) {
+    float e;
     if (ACT == SSA_ACT_SILU) return z * sigmoid<T>(z);
-    if (ACT == SSA_ACT_GELU) return z * normcdff(z);
+    if (ACT == SSA_ACT_GELU) return z * normal_cdf<T>(z, e);
     return z;
 }
 
+// z -> act'(z)
 template <typename T, int ACT>
 __device__ __forceinline__ float activate_grad(float z) {
     if (ACT == SSA_ACT_SILU) {
         const float t = sigmoid<T>(z);
         return t * fmaf(z, 1.0f - t, 1.0f);
     }
-    if (ACT == SSA_ACT_GELU) return fmaf(z * 0.3989422804014327f, expf(-0.5f * z * z), normcdff(z));
+    if (ACT == SSA_ACT_GELU) {
+        float e;
+        const float c = normal_cdf<T>(z, e);
+        return fmaf(z * 0.3989422804014327f, e, c);
+    }
     return 1.0f;
 }
 
@@ -288,127 +393,126 @@ __device__ __forceinline__ void wait_for_last_launch() { asm volatile("griddepco
 // ---- forward -----------------------------------------------------------------------------------
 
 // Sums of the tile's segments: per group of the column block, mean and squared deviations.
-template <typename T, int V>
+template <typename T, int A>
 __global__ void __launch_bounds__(kThreads) k_norm_stats(const __grid_constant__ NormArgs a) {
+    constexpr int V = Pieces<T, A>::V;
     extern __shared__ __align__(16) char smem[];
     float2* red = (float2*)smem;        // [rl][red_row], then the ring
     let_next_launch_start();
-    const uint32_t tile = blockIdx.x / a.blocks;
-    const Block b(a, blockIdx.x - tile * a.blocks, V);
-    if (tile == 0 && a.mean) {      // sequences without tokens have no tile
-        for (int s = threadIdx.x; s < a.B; s += kThreads)
-            if (a.seqs[s].hi == a.seqs[s].lo)
-                for (int g = b.g0; g <= b.g1; ++g) a.mean[(int64_t)s * a.G + g] = a.rstd[(int64_t)s * a.G + g] = 0.0f;
+    const uint32_t slot = blockIdx.x / a.blocks;
+    const Block b(a, blockIdx.x - slot * a.blocks, V);
+    const Tile tile(a, slot);
+    const int s = tile.s, n = tile.n, row_c = red_row(a, V);
+    if (n == 0) {
+        if (tile.tiles == 0 && a.mean)      // a sequence without tokens
+            for (int g = b.g0 + threadIdx.x; g <= b.g1; g += kThreads) a.mean[(int64_t)s * a.G + g] = a.rstd[(int64_t)s * a.G + g] = 0.0f;
+        return;
     }
-    for_segments(a, tile, [&](int s, int64_t t, int64_t e) {
-        const int n = (int)(e - t), row_c = red_row(a, V);
-        Rows<T, V, 1, kStages> rows = {{(const T*)a.x + (t + b.lane) * a.x_ts + b.channel(V)}, {a.rl * a.x_ts},
-                                       row_count(a, b, n), 0, smem + red_bytes(a, V)};
-        rows.start();
-        const int count = rows.count;
-        if (count) {
-            float p[V], sum[V], sq[V];      // p: the first row, negated
-            rows.peek(p);
+    Rows<T, A, 1, kStages> rows = {{(const T*)a.x + (tile.t0 + b.lane) * a.x_ts + b.c0 + b.vec * A}, {a.rl * a.x_ts},
+                                   row_count(a, b, n), b.chunks<A>(), b.nvec * A, smem + red_bytes(a, V)};
+    rows.start();
+    const int count = rows.count;
+    if (count) {
+        float p[V], sum[V], sq[V];      // p: the first row, negated
+        rows.peek(p);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                p[j] = -p[j];
-                sum[j] = sq[j] = 0.0f;
-            }
-            rows.each([&](const float (&e)[1][V]) {
-                if constexpr (V > 1) {
-#pragma unroll
-                    for (int j = 0; j < V; j += 2) {
-                        float d0, d1;
-                        add2(d0, d1, e[0][j], e[0][j + 1], p[j], p[j + 1]);
-                        add2(sum[j], sum[j + 1], sum[j], sum[j + 1], d0, d1);
-                        fma2(sq[j], sq[j + 1], d0, d1, d0, d1, sq[j], sq[j + 1]);
-                    }
-                } else {
-                    const float d = e[0][0] + p[0];
-                    sum[0] += d;
-                    sq[0] = fmaf(d, d, sq[0]);
-                }
-            });
-            const float inv = 1.0f / (float)count;
-            float2* mine = red + b.lane * row_c + b.vec * V;
-#pragma unroll
-            for (int j = 0; j < V; ++j) mine[j] = make_float2(fmaf(sum[j], inv, -p[j]), sq[j] - sum[j] * sum[j] * inv);
+        for (int j = 0; j < V; ++j) {
+            p[j] = -p[j];
+            sum[j] = sq[j] = 0.0f;
         }
-        __syncthreads();
-        // the channels' row lanes into row 0, then the groups' channels
-        const int less = n / a.rl, more = n - less * a.rl, lanes = min(a.rl, n);    // rows per lane; lanes with one more
-        for_channels(a, b, [&](int c, bool valid, int q, int Q) {
-            const float first = red[c].x;
-            float sum = 0.0f, sq = 0.0f;
-            for (int l = q; l < lanes; l += Q) {
-                const float2 v = red[l * row_c + c];
-                const float k = l < more ? less + 1.0f : (float)less, d = v.x - first;
-                sum = fmaf(k, d, sum);
-                sq += fmaf(k * d, d, v.y);
-            }
-            sum = lane_sum(sum, Q);
-            sq = lane_sum(sq, Q);
-            const float inv = 1.0f / (float)n;
-            if (q == 0 && valid) red[c] = make_float2(fmaf(sum, inv, first), sq - sum * sum * inv);
-        });
-        __syncthreads();
-        for_groups(a, b, [&](int g, int lo, int hi, int l, int L) {
-            const float first = lo < hi ? red[lo].x : 0.0f;
-            float sum = 0.0f, sq = 0.0f;
-            for (int c = lo + l; c < hi; c += L) {
-                const float d = red[c].x - first;
-                sum += d;
-                sq += fmaf(n * d, d, red[c].y);
-            }
-            sum = lane_sum(sum, L);
-            sq = lane_sum(sq, L);
-            if (l == 0 && lo < hi) {
-                const float d = sum / (float)(hi - lo);
-                a.group_part[((int64_t)(tile + s) * a.over + b.index - first_block(a, g, V)) * a.G + g] =
-                    make_float2(first + d, sq - n * sum * d);
+        rows.each([&](const float (&e)[1][V]) {
+#pragma unroll
+            for (int j = 0; j < V; j += 2) {
+                float d0, d1;
+                add2(d0, d1, e[0][j], e[0][j + 1], p[j], p[j + 1]);
+                add2(sum[j], sum[j + 1], sum[j], sum[j + 1], d0, d1);
+                fma2(sq[j], sq[j + 1], d0, d1, d0, d1, sq[j], sq[j + 1]);
             }
         });
-        __syncthreads();    // red is read
+        const float inv = 1.0f / (float)count;
+        float2* mine = red + b.lane * row_c;
+#pragma unroll
+        for (int j = 0; j < V; ++j) mine[b.relative<A>(j)] = make_float2(fmaf(sum[j], inv, -p[j]), sq[j] - sum[j] * sum[j] * inv);
+    }
+    __syncthreads();
+    // the channels' row lanes into row 0, then the groups' channels
+    const int less = n / a.rl, more = n - less * a.rl, lanes = min(a.rl, n);    // rows per lane; lanes with one more
+    for_channels(a, b, [&](int c, bool valid, int q, int Q) {
+        const float first = red[c].x;
+        float sum = 0.0f, sq = 0.0f;
+        for (int l = q; l < lanes; l += Q) {
+            const float2 v = red[l * row_c + c];
+            const float k = l < more ? less + 1.0f : (float)less, d = v.x - first;
+            sum = fmaf(k, d, sum);
+            sq += fmaf(k * d, d, v.y);
+        }
+        sum = lane_sum(sum, Q);
+        sq = lane_sum(sq, Q);
+        const float inv = 1.0f / (float)n;
+        if (q == 0 && valid) red[c] = make_float2(fmaf(sum, inv, first), sq - sum * sum * inv);
+    });
+    __syncthreads();
+    for_groups(a, b, [&](int g, int lo, int hi, int l, int L) {
+        const float first = lo < hi ? red[lo].x : 0.0f;
+        float sum = 0.0f, sq = 0.0f;
+        for (int c = lo + l; c < hi; c += L) {
+            const float d = red[c].x - first;
+            sum += d;
+            sq += fmaf(n * d, d, red[c].y);
+        }
+        sum = lane_sum(sum, L);
+        sq = lane_sum(sq, L);
+        if (l == 0 && lo < hi) {
+            const float d = sum / (float)(hi - lo);
+            a.group_part[((int64_t)slot * a.over + b.index - first_block(a, g, V)) * a.G + g] =
+                make_float2(first + d, sq - n * sum * d);
+        }
     });
 }
 
-// f(g, tile sums' table, first slot, slots, overlaps): one warp per group of the column block in sequence s.
+// f(g, lane, lanes) for the block's groups, several lanes of a warp to a group: all 32 for few groups, at least 4 for
+// many; all threads take part, those beyond the last group with group g1 and `valid` false.
 template <typename F>
-__device__ __forceinline__ void for_group_warps(const NormArgs& a, const Block& b, F f) {
-    for (int g = b.g0 + (threadIdx.x >> 5); g <= b.g1; g += kThreads / 32) f(g);
+__device__ __forceinline__ void for_merges(const Block& b, F f) {
+    const int groups = b.g1 - b.g0 + 1;
+    int L = 32;
+    while (L > 4 && kThreads / L < groups) L /= 2;
+    for (int base = b.g0; base <= b.g1; base += kThreads / L) {
+        const int g = base + threadIdx.x / L;
+        f(min(g, b.g1), g <= b.g1, threadIdx.x % L, L);
+    }
 }
 
-// Mean and rstd of the block's groups in sequence s into shared memory, from the tiles' in fp64 about the first
+// Mean and rstd of the block's groups in the tile's sequence into shared memory, from the tiles' in fp64 about the first
 // tile's mean.
-__device__ __forceinline__ void merge_stats(const NormArgs& a, const Block& b, int s, int V, bool write, float2* stats) {
-    const int lane = threadIdx.x & 31;
-    const int64_t lo = a.seqs[s].lo, hi = a.seqs[s].hi;
-    const int ta = (int)((uint32_t)lo / a.R), tiles = (int)((uint32_t)(hi - 1) / a.R) - ta + 1;
-    for_group_warps(a, b, [&](int g) {
+__device__ __forceinline__ void merge_stats(const NormArgs& a, const Block& b, const Tile& tile, int V, float2* stats) {
+    const int s = tile.s;
+    const int64_t tokens = a.seqs[s].hi - a.seqs[s].lo;
+    const uint32_t slot0 = first_slot(a, s);
+    for_merges(b, [&](int g, bool valid, int l, int L) {
         const int o0 = first_block(a, g, V), overlaps = last_block(a, g, V) - o0 + 1, cols = a.nv * V;
-        const float2* part = a.group_part + (int64_t)(ta + s) * a.over * a.G + g;
+        const float2* part = a.group_part + (int64_t)slot0 * a.over * a.G + g;
         const double first = part->x;
         double sum = 0.0, sq = 0.0;
         for (int o = 0; o < overlaps; ++o) {
             const int from = (o0 + o) * cols;
             const int c = min((g + 1) * a.width, from + cols) - max(g * a.width, from);    // its channels in the block
-#pragma unroll 4
-            for (int i = lane; i < tiles; i += 32) {
+#pragma unroll 8
+            for (int i = l; i < tile.tiles; i += L) {
                 const float2 v = part[((int64_t)i * a.over + o) * a.G];
-                const int64_t t = (int64_t)(ta + i) * a.R;
-                const double k = (double)((int)(min(hi, t + a.R) - max(lo, t)) * c), d = (double)v.x - first;
+                const double k = (double)((int)min((int64_t)a.R, tokens - (int64_t)i * a.R) * c), d = (double)v.x - first;
                 sum += k * d;
                 sq += (double)v.y + k * d * d;
             }
         }
-        sum = lane_sum(sum, 32);
-        sq = lane_sum(sq, 32);
-        const double m = (double)(hi - lo) * a.width, d = sum / m, var = fmax(sq / m - d * d, 0.0);
-        // a NaN or an infinity among the values leaves NaN here (fmax drops it)
-        const float mean = (float)(first + d), rstd = sq == sq ? (float)(1.0 / sqrt(var + (double)a.eps)) : (float)sq;
-        if (lane == 0) {
+        sum = lane_sum(sum, L);
+        sq = lane_sum(sq, L);
+        if (l == 0 && valid) {
+            const double m = (double)tokens * a.width, d = sum / m, var = fmax(sq / m - d * d, 0.0);
+            // a NaN or an infinity among the values leaves NaN here (fmax drops it)
+            const float mean = (float)(first + d), rstd = sq == sq ? (float)(1.0 / sqrt(var + (double)a.eps)) : (float)sq;
             stats[g - b.g0] = make_float2(mean, rstd);
-            if (write && a.mean && o0 == b.index) {
+            if (tile.opens && a.mean && o0 == b.index) {
                 a.mean[(int64_t)s * a.G + g] = mean;
                 a.rstd[(int64_t)s * a.G + g] = rstd;
             }
@@ -416,50 +520,47 @@ __device__ __forceinline__ void merge_stats(const NormArgs& a, const Block& b, i
     });
 }
 
-template <typename T, int V, int ACT>
+template <typename T, int A, int ACT>
 __global__ void __launch_bounds__(kThreads, 4) k_norm_apply(const __grid_constant__ NormArgs a) {
+    constexpr int V = Pieces<T, A>::V;
     extern __shared__ __align__(16) char smem[];
-    float2* stats = (float2*)(smem + Rows<T, V, 1, kStages>::kBytes);     // the block's groups, after the ring
-    const uint32_t i = gridDim.x - 1 - blockIdx.x, tile = i / a.blocks;
-    const Block b(a, i - tile * a.blocks, V);
-    for_segments(a, tile, [&](int s, int64_t t, int64_t e) {
-        const int c0 = b.channel(V);
-        Rows<T, V, 1, kStages> rows = {{(const T*)a.x + (t + b.lane) * a.x_ts + c0}, {a.rl * a.x_ts},
-                                       row_count(a, b, (int)(e - t)), 0, smem};
-        rows.start();
-        wait_for_last_launch();
-        merge_stats(a, b, s, V, t == a.seqs[s].lo, stats);
-        __syncthreads();
-        if (rows.count) {
-            float mean[V], scale[V], beta[V];       // mean: negated
+    float2* stats = (float2*)(smem + Rows<T, A, 1, kStages>::kBytes);     // the block's groups, after the ring
+    const uint32_t i = gridDim.x - 1 - blockIdx.x, slot = i / a.blocks;
+    const Block b(a, i - slot * a.blocks, V);
+    const Tile tile(a, slot);
+    if (tile.n == 0) return;
+    const int c0 = b.c0 + b.vec * A;
+    Rows<T, A, 1, kStages> rows = {{(const T*)a.x + (tile.t0 + b.lane) * a.x_ts + c0}, {a.rl * a.x_ts},
+                                   row_count(a, b, tile.n), b.chunks<A>(), b.nvec * A, smem};
+    rows.start();
+    wait_for_last_launch();
+    merge_stats(a, b, tile, V, stats);
+    __syncthreads();
+    if (rows.count) {
+        float mean[V], scale[V], beta[V];       // mean: negated
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float2 st = stats[group_of(a, c0 + j) - b.g0];
-                mean[j] = -st.x;
-                scale[j] = st.y * (a.gamma ? a.gamma[c0 + j] : 1.0f);
-                beta[j] = a.beta ? a.beta[c0 + j] : 0.0f;
-            }
-            const int64_t out_step = a.rl * a.o_ts;
-            T* out = (T*)a.out + (t + b.lane) * a.o_ts + c0;
-            rows.each([&](const float (&e)[1][V]) {
-                float z[V];
-                if constexpr (V > 1) {
-#pragma unroll
-                    for (int j = 0; j < V; j += 2) {
-                        add2(z[j], z[j + 1], e[0][j], e[0][j + 1], mean[j], mean[j + 1]);
-                        fma2(z[j], z[j + 1], z[j], z[j + 1], scale[j], scale[j + 1], beta[j], beta[j + 1]);
-                    }
-                } else {
-                    z[0] = fmaf(e[0][0] + mean[0], scale[0], beta[0]);
-                }
-#pragma unroll
-                for (int j = 0; j < V; ++j) z[j] = activate<T, ACT>(z[j]);
-                __stcs(reinterpret_cast<typename Vec<T, V>::C*>(out), Vec<T, V>::pack(z));
-                out += out_step;
-            });
+        for (int j = 0; j < V; ++j) {
+            const int c = b.channel<A>(j);
+            const float2 st = stats[group_of(a, c) - b.g0];
+            mean[j] = -st.x;
+            scale[j] = st.y * (a.gamma ? a.gamma[c] : 1.0f);
+            beta[j] = a.beta ? a.beta[c] : 0.0f;
         }
-        __syncthreads();    // stats are read
-    });
+        const int64_t out_step = a.rl * a.o_ts;
+        T* out = (T*)a.out + (tile.t0 + b.lane) * a.o_ts + c0;
+        rows.each([&](const float (&e)[1][V]) {
+            float z[V];
+#pragma unroll
+            for (int j = 0; j < V; j += 2) {
+                add2(z[j], z[j + 1], e[0][j], e[0][j + 1], mean[j], mean[j + 1]);
+                fma2(z[j], z[j + 1], z[j], z[j + 1], scale[j], scale[j + 1], beta[j], beta[j + 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) z[j] = activate<T, ACT>(z[j]);
+            Pieces<T, A>::store(out, z, rows.chunks, rows.hop);
+            out += out_step;
+        });
+    }
 }
 
 // ---- gradient ------------------------------------------------------------------------------------
@@ -469,13 +570,15 @@ __global__ void __launch_bounds__(kThreads, 4) k_norm_apply(const __grid_constan
 template <int V>
 struct Channels {
     float mean[V], scale[V], beta[V];
-    __device__ __forceinline__ void load(const NormArgs& a, int s, int c0) {
+    template <int A>
+    __device__ __forceinline__ void load(const NormArgs& a, const Block& b, int s) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const int64_t at = (int64_t)s * a.G + group_of(a, c0 + j);
+            const int c = b.channel<A>(j);
+            const int64_t at = (int64_t)s * a.G + group_of(a, c);
             mean[j] = -a.mean[at];
-            scale[j] = a.rstd[at] * (a.gamma ? a.gamma[c0 + j] : 1.0f);
-            beta[j] = a.beta ? a.beta[c0 + j] : 0.0f;
+            scale[j] = a.rstd[at] * (a.gamma ? a.gamma[c] : 1.0f);
+            beta[j] = a.beta ? a.beta[c] : 0.0f;
         }
     }
 };
@@ -483,129 +586,119 @@ struct Channels {
 // x - mean and dz of one row's vector: e = {x, dy}.
 template <typename T, int V, int ACT>
 __device__ __forceinline__ void row_grad(const Channels<V>& ch, const float (&e)[2][V], float (&xc)[V], float (&dz)[V]) {
-    if constexpr (V > 1) {
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-            add2(xc[j], xc[j + 1], e[0][j], e[0][j + 1], ch.mean[j], ch.mean[j + 1]);
-            if constexpr (ACT == SSA_ACT_NONE) {
-                dz[j] = e[1][j];
-                dz[j + 1] = e[1][j + 1];
-            } else {
-                float z0, z1;
-                fma2(z0, z1, xc[j], xc[j + 1], ch.scale[j], ch.scale[j + 1], ch.beta[j], ch.beta[j + 1]);
-                activate_grad2<T, ACT>(z0, z1);
-                mul2(dz[j], dz[j + 1], e[1][j], e[1][j + 1], z0, z1);
-            }
+    for (int j = 0; j < V; j += 2) {
+        add2(xc[j], xc[j + 1], e[0][j], e[0][j + 1], ch.mean[j], ch.mean[j + 1]);
+        if constexpr (ACT == SSA_ACT_NONE) {
+            dz[j] = e[1][j];
+            dz[j + 1] = e[1][j + 1];
+        } else {
+            float z0, z1;
+            fma2(z0, z1, xc[j], xc[j + 1], ch.scale[j], ch.scale[j + 1], ch.beta[j], ch.beta[j + 1]);
+            activate_grad2<T, ACT>(z0, z1);
+            mul2(dz[j], dz[j + 1], e[1][j], e[1][j + 1], z0, z1);
         }
-    } else {
-        xc[0] = e[0][0] + ch.mean[0];
-        dz[0] = e[1][0] * activate_grad<T, ACT>(fmaf(xc[0], ch.scale[0], ch.beta[0]));
     }
 }
 
-template <typename T, int V>
-__device__ __forceinline__ Rows<T, V, 2, kGradStages> grad_rows(const NormArgs& a, const Block& b, int64_t t, int n, char* ring) {
-    return {{(const T*)a.x + (t + b.lane) * a.x_ts + b.channel(V), (const T*)a.dy + (t + b.lane) * a.dy_ts + b.channel(V)},
-            {a.rl * a.x_ts, a.rl * a.dy_ts}, row_count(a, b, n), 0, ring};
+template <typename T, int A>
+__device__ __forceinline__ Rows<T, A, 2, kGradStages> grad_rows(const NormArgs& a, const Block& b, const Tile& tile, char* ring) {
+    const int64_t row = tile.t0 + b.lane;
+    const int c0 = b.c0 + b.vec * A;
+    return {{(const T*)a.x + row * a.x_ts + c0, (const T*)a.dy + row * a.dy_ts + c0},
+            {a.rl * a.x_ts, a.rl * a.dy_ts}, row_count(a, b, tile.n), b.chunks<A>(), b.nvec * A, ring};
 }
 
-// Sums of the tile's segments: per channel dz and dz * xhat, per group of the column block the same times gamma.
-template <typename T, int V, int ACT>
+// Sums of a tile: per channel dz and dz * xhat, per group of the column block the same times gamma.
+template <typename T, int A, int ACT>
 __global__ void __launch_bounds__(kThreads, 2) k_norm_grad_sums(const __grid_constant__ NormArgs a) {
+    constexpr int V = Pieces<T, A>::V;
     extern __shared__ __align__(16) char smem[];
     float2* red = (float2*)smem;
     let_next_launch_start();
-    const uint32_t tile = blockIdx.x / a.blocks;
-    const Block b(a, blockIdx.x - tile * a.blocks, V);
-    for_segments(a, tile, [&](int s, int64_t t, int64_t e) {
-        const int n = (int)(e - t), row_c = red_row(a, V), lanes = min(a.rl, n);
-        auto rows = grad_rows<T, V>(a, b, t, n, smem + red_bytes(a, V));
-        rows.start();
-        if (rows.count) {
-            Channels<V> ch;
-            ch.load(a, s, b.channel(V));
-            float s0[V], s1[V];
+    const uint32_t slot = blockIdx.x / a.blocks;
+    const Block b(a, blockIdx.x - slot * a.blocks, V);
+    const Tile tile(a, slot);
+    const int s = tile.s, n = tile.n, row_c = red_row(a, V), lanes = min(a.rl, n);
+    if (n == 0) return;
+    auto rows = grad_rows<T, A>(a, b, tile, smem + red_bytes(a, V));
+    rows.start();
+    if (rows.count) {
+        Channels<V> ch;
+        ch.template load<A>(a, b, s);
+        float s0[V], s1[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) s0[j] = s1[j] = 0.0f;
-            rows.each([&](const float (&e)[2][V]) {
-                float xc[V], dz[V];
-                row_grad<T, V, ACT>(ch, e, xc, dz);
-                if constexpr (V > 1) {
+        for (int j = 0; j < V; ++j) s0[j] = s1[j] = 0.0f;
+        rows.each([&](const float (&e)[2][V]) {
+            float xc[V], dz[V];
+            row_grad<T, V, ACT>(ch, e, xc, dz);
 #pragma unroll
-                    for (int j = 0; j < V; j += 2) {
-                        add2(s0[j], s0[j + 1], s0[j], s0[j + 1], dz[j], dz[j + 1]);
-                        fma2(s1[j], s1[j + 1], dz[j], dz[j + 1], xc[j], xc[j + 1], s1[j], s1[j + 1]);
-                    }
-                } else {
-                    s0[0] += dz[0];
-                    s1[0] = fmaf(dz[0], xc[0], s1[0]);
-                }
-            });
-            float2* mine = red + b.lane * row_c + b.vec * V;
+            for (int j = 0; j < V; j += 2) {
+                add2(s0[j], s0[j + 1], s0[j], s0[j + 1], dz[j], dz[j + 1]);
+                fma2(s1[j], s1[j + 1], dz[j], dz[j + 1], xc[j], xc[j + 1], s1[j], s1[j + 1]);
+            }
+        });
+        float2* mine = red + b.lane * row_c;
 #pragma unroll
-            for (int j = 0; j < V; ++j) mine[j] = make_float2(s0[j], s1[j]);
+        for (int j = 0; j < V; ++j) mine[b.relative<A>(j)] = make_float2(s0[j], s1[j]);
+    }
+    __syncthreads();
+    for_channels(a, b, [&](int c, bool valid, int q, int Q) {
+        float s0 = 0.0f, s1 = 0.0f;
+        for (int l = q; l < lanes; l += Q) {
+            const float2 v = red[l * row_c + c];
+            s0 += v.x;
+            s1 += v.y;
         }
-        __syncthreads();
-        for_channels(a, b, [&](int c, bool valid, int q, int Q) {
-            float s0 = 0.0f, s1 = 0.0f;
-            for (int l = q; l < lanes; l += Q) {
-                const float2 v = red[l * row_c + c];
-                s0 += v.x;
-                s1 += v.y;
-            }
-            s0 = lane_sum(s0, Q);
-            s1 = lane_sum(s1, Q);
-            if (q == 0 && valid) {
-                s1 *= a.rstd[(int64_t)s * a.G + group_of(a, b.c0 + c)];
-                a.chan_part[(int64_t)(tile + s) * a.C + b.c0 + c] = make_float2(s0, s1);
-                const float gamma = a.gamma ? a.gamma[b.c0 + c] : 1.0f;
-                red[c] = make_float2(s0 * gamma, s1 * gamma);
-            }
-        });
-        __syncthreads();
-        for_groups(a, b, [&](int g, int lo, int hi, int l, int L) {
-            float s1 = 0.0f, s2 = 0.0f;
-            for (int c = lo + l; c < hi; c += L) {
-                s1 += red[c].x;
-                s2 += red[c].y;
-            }
-            s1 = lane_sum(s1, L);
-            s2 = lane_sum(s2, L);
-            if (l == 0 && lo < hi)
-                a.group_part[((int64_t)(tile + s) * a.over + b.index - first_block(a, g, V)) * a.G + g] = make_float2(s1, s2);
-        });
-        __syncthreads();
+        s0 = lane_sum(s0, Q);
+        s1 = lane_sum(s1, Q);
+        if (q == 0 && valid) {
+            s1 *= a.rstd[(int64_t)s * a.G + group_of(a, b.c0 + c)];
+            a.chan_part[(int64_t)slot * a.C + b.c0 + c] = make_float2(s0, s1);
+            const float gamma = a.gamma ? a.gamma[b.c0 + c] : 1.0f;
+            red[c] = make_float2(s0 * gamma, s1 * gamma);
+        }
+    });
+    __syncthreads();
+    for_groups(a, b, [&](int g, int lo, int hi, int l, int L) {
+        float s1 = 0.0f, s2 = 0.0f;
+        for (int c = lo + l; c < hi; c += L) {
+            s1 += red[c].x;
+            s2 += red[c].y;
+        }
+        s1 = lane_sum(s1, L);
+        s2 = lane_sum(s2, L);
+        if (l == 0 && lo < hi)
+            a.group_part[((int64_t)slot * a.over + b.index - first_block(a, g, V)) * a.G + g] = make_float2(s1, s2);
     });
 }
 
 // rstd * S1 and rstd^2 * S2, negated, of the block's groups in sequence s into shared memory.
-__device__ __forceinline__ void merge_sums(const NormArgs& a, const Block& b, int s, int V, float2* sums) {
-    const int lane = threadIdx.x & 31;
-    const int64_t lo = a.seqs[s].lo, hi = a.seqs[s].hi;
-    const int ta = (int)((uint32_t)lo / a.R), tiles = (int)((uint32_t)(hi - 1) / a.R) - ta + 1;
-    for_group_warps(a, b, [&](int g) {
+__device__ __forceinline__ void merge_sums(const NormArgs& a, const Block& b, const Tile& tile, int V, float2* sums) {
+    const int s = tile.s;
+    const uint32_t slot0 = first_slot(a, s);
+    for_merges(b, [&](int g, bool valid, int l, int L) {
         const int overlaps = last_block(a, g, V) - first_block(a, g, V) + 1;
-        const float2* part = a.group_part + (int64_t)(ta + s) * a.over * a.G + g;
+        const float2* part = a.group_part + (int64_t)slot0 * a.over * a.G + g;
         double s1 = 0.0, s2 = 0.0;
         for (int o = 0; o < overlaps; ++o) {
-#pragma unroll 4
-            for (int i = lane; i < tiles; i += 32) {
+#pragma unroll 8
+            for (int i = l; i < tile.tiles; i += L) {
                 const float2 v = part[((int64_t)i * a.over + o) * a.G];
                 s1 += v.x;
                 s2 += v.y;
             }
         }
-        s1 = lane_sum(s1, 32);
-        s2 = lane_sum(s2, 32);
-        if (lane == 0) {
-            const double r = a.rstd[(int64_t)s * a.G + g], f = -r / ((double)(hi - lo) * a.width);
+        s1 = lane_sum(s1, L);
+        s2 = lane_sum(s2, L);
+        if (l == 0 && valid) {
+            const double r = a.rstd[(int64_t)s * a.G + g], f = -r / ((double)(a.seqs[s].hi - a.seqs[s].lo) * a.width);
             sums[g - b.g0] = make_float2((float)(f * s1), (float)(f * r * s2));
         }
     });
 }
 
-// The weights' gradients of 32 channels: the sums of all slots, in fp64. Slots that no segment has (a tile without
-// tokens of the sequence) are skipped: slot i belongs to sequence s where i - s is one of its tiles.
+// The weights' gradients of 32 channels: the sums of all tiles, in fp64.
 __device__ __forceinline__ void merge_weights(const NormArgs& a, int c0, double2* red) {
     const int c = c0 + (threadIdx.x & 31), w = threadIdx.x >> 5;
     double2 acc = make_double2(0.0, 0.0);
@@ -613,7 +706,7 @@ __device__ __forceinline__ void merge_weights(const NormArgs& a, int c0, double2
         for (int s = 0; s < a.B; ++s) {
             const int64_t lo = a.seqs[s].lo, hi = a.seqs[s].hi;
             if (hi <= lo) continue;
-            const int64_t from = (uint32_t)lo / a.R + s, to = (uint32_t)(hi - 1) / a.R + s;
+            const int64_t from = first_slot(a, s), to = from + (uint32_t)(hi - lo - 1) / a.R;
 #pragma unroll 4
             for (int64_t i = from + w; i <= to; i += kThreads / 32) {
                 const float2 v = a.chan_part[i * a.C + c];
@@ -635,55 +728,52 @@ __device__ __forceinline__ void merge_weights(const NormArgs& a, int c0, double2
 }
 
 // dx, the tiles in reverse; the first CTAs add up the weights' gradients, 32 channels each.
-template <typename T, int V, int ACT>
+template <typename T, int A, int ACT>
 __global__ void __launch_bounds__(kThreads, 2) k_norm_grad_apply(const __grid_constant__ NormArgs a) {
+    constexpr int V = Pieces<T, A>::V;
     extern __shared__ __align__(16) char smem[];
-    float2* sums = (float2*)(smem + Rows<T, V, 2, kGradStages>::kBytes);
+    float2* sums = (float2*)(smem + Rows<T, A, 2, kGradStages>::kBytes);
     const uint32_t weights = (a.C + 31) / 32;
     if (blockIdx.x < weights) {
         wait_for_last_launch();
         merge_weights(a, blockIdx.x * 32, (double2*)smem);
         return;
     }
-    const uint32_t i = gridDim.x - 1 - blockIdx.x, tile = i / a.blocks;
-    const Block b(a, i - tile * a.blocks, V);
-    for_segments(a, tile, [&](int s, int64_t t, int64_t e) {
-        auto rows = grad_rows<T, V>(a, b, t, (int)(e - t), smem);
-        rows.start();
-        wait_for_last_launch();
-        merge_sums(a, b, s, V, sums);
-        __syncthreads();
-        if (rows.count) {
-            const int c0 = b.channel(V);
-            Channels<V> ch;
-            ch.load(a, s, c0);
-            float S1[V], S2[V];
+    const uint32_t i = gridDim.x - 1 - blockIdx.x, slot = i / a.blocks;
+    const Block b(a, i - slot * a.blocks, V);
+    const Tile tile(a, slot);
+    const int s = tile.s;
+    if (tile.n == 0) return;
+    auto rows = grad_rows<T, A>(a, b, tile, smem);
+    rows.start();
+    wait_for_last_launch();
+    merge_sums(a, b, tile, V, sums);
+    __syncthreads();
+    if (rows.count) {
+        const int c0 = b.c0 + b.vec * A;
+        Channels<V> ch;
+        ch.template load<A>(a, b, s);
+        float S1[V], S2[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float2 v = sums[group_of(a, c0 + j) - b.g0];
-                S1[j] = v.x;
-                S2[j] = v.y;
-            }
-            const int64_t out_step = a.rl * a.o_ts;
-            T* out = (T*)a.out + (t + b.lane) * a.o_ts + c0;
-            rows.each([&](const float (&e)[2][V]) {
-                float xc[V], dz[V];
-                row_grad<T, V, ACT>(ch, e, xc, dz);
-                if constexpr (V > 1) {
-#pragma unroll
-                    for (int j = 0; j < V; j += 2) {
-                        fma2(dz[j], dz[j + 1], dz[j], dz[j + 1], ch.scale[j], ch.scale[j + 1], S1[j], S1[j + 1]);
-                        fma2(dz[j], dz[j + 1], xc[j], xc[j + 1], S2[j], S2[j + 1], dz[j], dz[j + 1]);
-                    }
-                } else {
-                    dz[0] = fmaf(dz[0], ch.scale[0], fmaf(xc[0], S2[0], S1[0]));
-                }
-                __stcs(reinterpret_cast<typename Vec<T, V>::C*>(out), Vec<T, V>::pack(dz));
-                out += out_step;
-            });
+        for (int j = 0; j < V; ++j) {
+            const float2 v = sums[group_of(a, b.channel<A>(j)) - b.g0];
+            S1[j] = v.x;
+            S2[j] = v.y;
         }
-        __syncthreads();
-    });
+        const int64_t out_step = a.rl * a.o_ts;
+        T* out = (T*)a.out + (tile.t0 + b.lane) * a.o_ts + c0;
+        rows.each([&](const float (&e)[2][V]) {
+            float xc[V], dz[V];
+            row_grad<T, V, ACT>(ch, e, xc, dz);
+#pragma unroll
+            for (int j = 0; j < V; j += 2) {
+                fma2(dz[j], dz[j + 1], dz[j], dz[j + 1], ch.scale[j], ch.scale[j + 1], S1[j], S1[j + 1]);
+                fma2(dz[j], dz[j + 1], xc[j], xc[j + 1], S2[j], S2[j + 1], dz[j], dz[j + 1]);
+            }
+            Pieces<T, A>::store(out, dz, rows.chunks, rows.hop);
+            out += out_step;
+        });
+    }
 }
 
 // ---- host --------------------------------------------------------------------------------------
@@ -693,13 +783,14 @@ using Kernel = std::integral_constant<void (*)(NormArgs), K>;
 
 struct Launch {
     bool grad;
-    int act, V, device;
+    int act, A, device;     // A: elements per chunk
     cudaStream_t st;
 };
 
-template <typename T, int V, int ACT>
+template <typename T, int A, int ACT>
 bool launch_act(const NormArgs& a, const Launch& l) {
-    const unsigned grid = a.tiles * (unsigned)a.blocks;
+    constexpr int V = Pieces<T, A>::V;
+    const unsigned grid = a.slots * (unsigned)a.blocks;
     const size_t red = red_bytes(a, V), groups = sizeof(float2) * std::min(a.G, a.nv * V);    // at most 16 KB each
     auto go = [&](auto tag, unsigned ctas, size_t smem, bool second) {
         constexpr auto kernel = decltype(tag)::value;
@@ -718,38 +809,38 @@ bool launch_act(const NormArgs& a, const Launch& l) {
         return cudaLaunchKernelEx(&config, kernel, a) == cudaSuccess;
     };
     if (l.grad) {
-        const size_t ring = Rows<T, V, 2, kGradStages>::kBytes;
-        return go(Kernel<k_norm_grad_sums<T, V, ACT>>(), grid, red + ring, false) &&
-               go(Kernel<k_norm_grad_apply<T, V, ACT>>(), grid + (unsigned)cdiv(a.C, 32), std::max(ring + groups, sizeof(double2) * kThreads), true);
+        const size_t ring = Rows<T, A, 2, kGradStages>::kBytes;
+        return go(Kernel<k_norm_grad_sums<T, A, ACT>>(), grid, red + ring, false) &&
+               go(Kernel<k_norm_grad_apply<T, A, ACT>>(), grid + (unsigned)cdiv(a.C, 32), std::max(ring + groups, sizeof(double2) * kThreads), true);
     }
-    const size_t ring = Rows<T, V, 1, kStages>::kBytes;
-    return go(Kernel<k_norm_stats<T, V>>(), grid, red + ring, false) && go(Kernel<k_norm_apply<T, V, ACT>>(), grid, ring + groups, true);
+    const size_t ring = Rows<T, A, 1, kStages>::kBytes;
+    return go(Kernel<k_norm_stats<T, A>>(), grid, red + ring, false) && go(Kernel<k_norm_apply<T, A, ACT>>(), grid, ring + groups, true);
 }
 
-template <typename T, int V>
-bool launch_vec(const NormArgs& a, const Launch& l) {
-    if (l.act == SSA_ACT_SILU) return launch_act<T, V, SSA_ACT_SILU>(a, l);
-    if (l.act == SSA_ACT_GELU) return launch_act<T, V, SSA_ACT_GELU>(a, l);
-    return launch_act<T, V, SSA_ACT_NONE>(a, l);
+template <typename T, int A>
+bool launch_chunk(const NormArgs& a, const Launch& l) {
+    if (l.act == SSA_ACT_SILU) return launch_act<T, A, SSA_ACT_SILU>(a, l);
+    if (l.act == SSA_ACT_GELU) return launch_act<T, A, SSA_ACT_GELU>(a, l);
+    return launch_act<T, A, SSA_ACT_NONE>(a, l);
 }
 
 template <typename T>
 bool launch_type(const NormArgs& a, const Launch& l) {
     if constexpr (sizeof(T) == 2) {
-        if (l.V == 8) return launch_vec<T, 8>(a, l);
+        if (l.A == 8) return launch_chunk<T, 8>(a, l);
     }
-    if (l.V == 4) return launch_vec<T, 4>(a, l);
-    if (l.V == 2) return launch_vec<T, 2>(a, l);
-    return launch_vec<T, 1>(a, l);
+    if (l.A == 4) return launch_chunk<T, 4>(a, l);
+    if (l.A == 2) return launch_chunk<T, 2>(a, l);
+    return launch_chunk<T, 1>(a, l);
 }
 
 // Column blocks and tiles of a call.
-void shape(NormArgs& a, int V, size_t es, int ctas) {
-    a.nvt = a.C / V;
-    // vectors per block: at least kBlockBytes of a row, the narrowest that keeps nine tenths of the threads on vectors
-    const int least = std::min<int>(a.nvt, std::max<int>(1, kBlockBytes / (V * (int)es)));
+void shape(NormArgs& a, int V, int chunk, int ctas) {
+    a.nvt = (int32_t)cdiv(a.C, V);
+    // vectors per block: at least kBlockBytes of a row in a round of chunks, the narrowest that keeps nine tenths of the threads on vectors
+    const int least = std::min(a.nvt, kBlockBytes / chunk);
     int best = -1;
-    for (int n = least; n <= std::min(a.nvt, std::max(least, 4 * least)) && n <= kThreads; ++n) {
+    for (int n = least; n <= std::min(a.nvt, 4 * least); ++n) {
         const int used = (int)((int64_t)100 * a.nvt * (kThreads / n) / (cdiv(a.nvt, n) * kThreads));
         if (used > best) {
             best = used;
@@ -764,10 +855,11 @@ void shape(NormArgs& a, int V, size_t es, int ctas) {
     while (a.clanes < 32 && a.clanes * 2 <= a.rl && a.clanes * 2 * a.nv * V <= kThreads) a.clanes *= 2;
     while (a.glanes < 32 && a.glanes < std::min(a.width, a.nv * V)) a.glanes *= 2;
     a.magic = (uint32_t)((((uint64_t)1 << 32) + a.width - 1) / a.width);
-    // tokens per tile, a multiple of the row lanes: kRowsPerThread a thread, less where that leaves SMs without CTAs
-    const int64_t even = cdiv(a.N, std::max<int64_t>(1, ctas / a.blocks));
-    a.R = (uint32_t)(a.rl * std::min<int64_t>(kRowsPerThread, cdiv(even, a.rl)));
-    a.tiles = (uint32_t)cdiv(a.N, a.R);
+    // tokens per tile, a multiple of the row lanes: kRowsPerThread a thread; less where that leaves SMs without CTAs, but
+    // not for more than kMaxTiles tiles, whose sums every CTA of the second pass adds up
+    const int64_t tiles = std::min<int64_t>(kMaxTiles, std::max(1, ctas / a.blocks));
+    a.R = (uint32_t)(a.rl * std::min<int64_t>(kRowsPerThread, cdiv(cdiv(a.N, tiles), a.rl)));
+    a.slots = (uint32_t)(a.N / a.R + a.B);
 }
 
 struct Call {
@@ -801,11 +893,9 @@ ssa_status_t run_norm(Plan* p, const Call& c, int32_t C, int32_t G, float eps, i
     for (const ssa_heads_t* in : {&x, &dy})
         if (!same_view(out, *in, N) && !disjoint(out, *in, N, C, es)) return SSA_ERR_INVALID_ARG;
 
-    int V = dt == SSA_F32 ? 4 : 8;
-    while (V > 1 && C % V) V >>= 1;
-    V = view_vector(x, N, es, V);
-    V = view_vector(dy, N, es, V);
-    V = view_vector(out, N, es, V);
+    int A = kVecBytes / (int)es;
+    while (A > 1 && C % A) A >>= 1;
+    for (const ssa_heads_t* v : {&x, &dy, &out}) A = view_vector(*v, N, es, A);
     NormArgs a = {};
     a.x = x.data;
     a.dy = dy.data;
@@ -826,16 +916,16 @@ ssa_status_t run_norm(Plan* p, const Call& c, int32_t C, int32_t G, float eps, i
     a.eps = eps;
     const DeviceScope on(p->device);
     if (!on.ok) return SSA_ERR_CUDA;
-    shape(a, V, es, (grad ? 2 : 4) * sm_count(p->device));
-    if ((int64_t)a.tiles * a.blocks >= ((int64_t)1 << 30)) return SSA_ERR_UNSUPPORTED;
+    shape(a, kVecBytes / (int)es, A * (int)es, (grad ? 2 : 4) * sm_count(p->device));
+    if ((int64_t)a.slots * a.blocks >= ((int64_t)1 << 30)) return SSA_ERR_UNSUPPORTED;
     // one buffer of the tiles' sums
-    const int64_t slots = (int64_t)a.tiles + p->B, n_group = slots * a.over * G, n_chan = grad ? slots * C : 0;
+    const int64_t n_group = (int64_t)a.slots * a.over * G, n_chan = grad ? (int64_t)a.slots * C : 0;
     a.group_part = (float2*)p->alloc(sizeof(float2) * (size_t)(n_group + n_chan), st, p->alloc_ctx);
     if (!a.group_part) return SSA_ERR_ALLOC;
     a.chan_part = a.group_part + n_group;
     a.mean = c.mean;
     a.rstd = c.rstd;
-    const Launch l = {grad, act, V, p->device, st};
+    const Launch l = {grad, act, A, p->device, st};
     const bool ok = dt == SSA_F32    ? launch_type<float>(a, l)
                     : dt == SSA_BF16 ? launch_type<__nv_bfloat16>(a, l)
                                      : launch_type<__half>(a, l);

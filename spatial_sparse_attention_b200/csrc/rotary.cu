@@ -37,6 +37,7 @@ struct RowsArg {
     float* part;          // gradient with weights: [CTAs of this tensor][D] partial sums
     int64_t x_ts, x_hs, g_ts, g_hs, o_ts, o_hs;
     int32_t H;
+    int32_t tile;         // gradient: tokens per tile
 };
 
 // Frequencies as fractions of a turn in units of 2^-64: coordinate * turns wraps modulo one turn by
@@ -47,7 +48,7 @@ struct RotArgs {
     int64_t N;
     int32_t D, G;                  // head dimension; lanes per row
     int32_t pairs;                 // rotated pairs
-    int32_t tile;                  // tokens per tile
+    int32_t tile;                  // tokens per tile (gradient: the larger of the two)
     int32_t device;                // host side
     int32_t ctas0;                 // gradient: CTAs [0, ctas0) work on t[0], the rest on t[1]
     float eps, inv_d, mscale, sgn; // inv_d = 1/D; sgn = -1 turns back
@@ -412,14 +413,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_rotary_grad(const __grid_consta
     const int H = t.H, step = kWarps * rpw, dt = step / H, dh = step - dt * H;
     const int r0 = (threadIdx.x >> 5) * rpw;
     const Cursor first = {r0 + sub, (r0 + sub) / H, (r0 + sub) % H};
-    const int64_t stride = (int64_t)nctas * a.tile;
+    const int64_t stride = (int64_t)nctas * t.tile;
     // what is fetched next: row `ahead` of the tile at `ftok`, in steps of the whole CTA
-    int64_t ftok = (int64_t)cta * a.tile;
+    int64_t ftok = (int64_t)cta * t.tile;
     int frow = 0, fbase = 0;
     Cursor ahead = first;
     auto fetch = [&](int stage) {
         if (ftok < a.N) {
-            if (fbase == 0) frow = (int)min((int64_t)a.tile, a.N - ftok) * H;
+            if (fbase == 0) frow = (int)min((int64_t)t.tile, a.N - ftok) * H;
             if (ahead.r < frow && sub < rpw) {
                 fetch_row<CUT, T>(smem, stage, (const T*)t.x + (ftok + ahead.t) * t.x_ts + ahead.h * t.x_hs, off);
                 fetch_row<CUT, T>(ring_g, stage, (const T*)t.g + (ftok + ahead.t) * t.g_ts + ahead.h * t.g_hs, off);
@@ -441,8 +442,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_rotary_grad(const __grid_consta
     float gam[E];
     read_gamma<CUT>(gamma, l, G, gam);
     int stage = 0;
-    for (int64_t tok0 = (int64_t)cta * a.tile; tok0 < a.N; tok0 += stride) {
-        const int ntok = (int)min((int64_t)a.tile, a.N - tok0);
+    for (int64_t tok0 = (int64_t)cta * t.tile; tok0 < a.N; tok0 += stride) {
+        const int ntok = (int)min((int64_t)t.tile, a.N - tok0);
         __syncthreads();    // the previous tile's tables are read
         fill_tables<CUT::P>(a, tok0, ntok, cs, sn);
         __syncthreads();
@@ -685,7 +686,7 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
         const ssa_heads_t* g = grad ? c.g[i] : x;
         t = RowsArg{x->data, g->data, c.out[i]->data, norm ? c.gamma[i] : nullptr, nullptr,
                     x->token_stride, x->head_stride, g->token_stride, g->head_stride,
-                    c.out[i]->token_stride, c.out[i]->head_stride, x->heads};
+                    c.out[i]->token_stride, c.out[i]->head_stride, x->heads, 0};
     }
     a.coords = p->coords;
     a.N = N;
@@ -702,8 +703,17 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
     const int sms = sm_count(p->device);
     // tokens per tile: some 1280 rows, so that the start of a CTA is a small part of it, but eight CTAs per SM; and
     // the rows that the CTA's warps take at once
-    const int heads = a.t[0].H + (grad ? 0 : a.t[1].H), once = kWarps * (32 / a.G);
-    a.tile = (int)std::min<int64_t>({(int64_t)kMaxTile, cdiv(1280, heads), std::max(cdiv(once, heads), cdiv(N, 8 * sms))});
+    const int once = kWarps * (32 / a.G);
+    auto tile_of = [&](int heads) {
+        return (int)std::min<int64_t>({(int64_t)kMaxTile, cdiv(1280, heads), std::max(cdiv(once, heads), cdiv(N, 8 * sms))});
+    };
+    if (grad) {
+        a.t[0].tile = tile_of(a.t[0].H);
+        a.t[1].tile = nt == 2 ? tile_of(a.t[1].H) : 0;
+        a.tile = std::max(a.t[0].tile, a.t[1].tile);
+    } else {
+        a.tile = tile_of(a.t[0].H + a.t[1].H);
+    }
     const int64_t tiles = cdiv(N, a.tile);
     ssa_status_t out = SSA_OK;
     if (!grad) {
@@ -711,8 +721,8 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
     } else {
         // persistent CTAs, shared out by the tensors' heads
         const int64_t most = 2 * sms, hq = a.t[0].H, hk = a.t[1].H;
-        const int n0 = (int)std::min(tiles, std::max<int64_t>(1, most * hq / (hq + hk)));
-        const int n1 = nt == 2 ? (int)std::min(tiles, std::max<int64_t>(1, most * hk / (hq + hk))) : 0;
+        const int n0 = (int)std::min(cdiv(N, a.t[0].tile), std::max<int64_t>(1, most * hq / (hq + hk)));
+        const int n1 = nt == 2 ? (int)std::min(cdiv(N, a.t[1].tile), std::max<int64_t>(1, most * hk / (hq + hk))) : 0;
         float* part = (float*)p->alloc(sizeof(float) * (size_t)(n0 + n1) * D, st, p->alloc_ctx);
         if (!part) {
             out = SSA_ERR_ALLOC;
