@@ -34,7 +34,8 @@ constexpr int kMaxChannels = 65536;
 // the cancellation is at most a factor n, as the pivot is one of them (sq <= n D^2, D the largest deviation from it, and
 // the squared deviations from the mean are at least D^2 / 2).
 constexpr int kRowsPerThread = 48;
-constexpr int kMaxTiles = 148;
+constexpr int kTilesPerLane = 10;       // tiles of a column that one lane of a merge adds up,
+constexpr int kMinTiles = 148;          // where that does not leave SMs without work
 constexpr int kBlockBytes = 128;        // of a row that a column block's threads read together, at least
 constexpr int kStages = 8;              // rows per thread in flight or in use: forward, gradient
 constexpr int kGradStages = 6;
@@ -307,44 +308,53 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// sigma(z). The 16-bit types take the hardware's exponential and reciprocal (2^-20 relative for |z| < 16, far
-// below their rounding); fp32 the exact functions.
+// 2^(c x) for a constant c = hi + lo, to the hardware's 2 ulp whatever the size of c x: what rounding takes from the
+// product comes back as a factor. |c x| < 300.
+__device__ __forceinline__ float ex2_scaled(float x, float hi, float lo) {
+    const float y = x * hi, rest = fmaf(x, lo, fmaf(x, hi, -y)), e = ex2(y);
+    return fmaf(e, rest * 0.6931472f, e);
+}
+
+// sigma(z), by the hardware's exponential and reciprocal. For the 16-bit types the exponent's product is rounded
+// (2^-20 relative for |z| < 16, far below theirs); with expf and a division fp32 would wait for instructions, not memory.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float z) {
-    return rcp(1.0f + ex2(z * -1.4426950408889634f));
-}
-template <>
-__device__ __forceinline__ float sigmoid<float>(float z) {
-    return 1.0f / (1.0f + expf(-z));
+    if constexpr (sizeof(T) == 2) return rcp(1.0f + ex2(z * -1.4426950408889634f));
+    return rcp(1.0f + ex2_scaled(fminf(fmaxf(z, -88.0f), 88.0f), -1.44269502f, -1.92596303e-8f));
 }
 
-// Phi(-|z|) of the normal distribution, as t p(t) exp(-z^2 / 2) with t = 1 / (1 + 0.3 |z|): p fitted to the scaled complement
-// erfc(x) exp(x^2) / 2 at x = |z| / sqrt(2) <= 10 for least relative error, 3.4e-7 in fp32. For the 16-bit types; `e`
-// is exp(-z^2 / 2), which the gradient needs as well. normcdff, twice as many instructions, bounds the pass that writes
-// in place of memory (570 against 290 us for 135,000 tokens x 1376 bf16); fp32 keeps it.
-__device__ __forceinline__ float normal_tail(float z, float e) {
-    const float t = rcp(fmaf(fabsf(z), 0.3f, 1.0f));
-    float p = fmaf(t, 0.035675015f, -0.157204f);
-    p = fmaf(p, t, 0.20635495f);
-    p = fmaf(p, t, -0.053684855f);
-    p = fmaf(p, t, 0.12856221f);
-    p = fmaf(p, t, 0.09991333f);
-    p = fmaf(p, t, 0.12075398f);
-    p = fmaf(p, t, 0.11962929f);
-    return p * t * e;
-}
-
-// Phi(z) and exp(-z^2 / 2).
+// Phi(z) of the normal distribution, and e = exp(-z^2 / 2). Phi(-|z|) is t p(t) e with t = 1 / (1 + a |z|): p is fitted to
+// the scaled complement erfc(x) exp(x^2) / 2 at x = |z| / sqrt(2) <= 10 for least relative error, of degree 7 (3.4e-7 in
+// fp32) for the 16-bit types and 8 (2.3e-7, the fp32 evaluation's own) for fp32. normcdff, twice as many instructions, bounds the
+// pass that writes in place of memory (570 against 242 us for 135,000 tokens x 1376 bf16).
 template <typename T>
 __device__ __forceinline__ float normal_cdf(float z, float& e) {
+    float q;
     if constexpr (sizeof(T) == 2) {
         e = ex2(z * z * -0.72134752f);      // log2(e) / 2
-        const float q = normal_tail(z, e);
-        return z > 0.0f ? 1.0f - q : q;
+        const float t = rcp(fmaf(fabsf(z), 0.3f, 1.0f));
+        float p = fmaf(t, 0.035675015f, -0.157204f);
+        p = fmaf(p, t, 0.20635495f);
+        p = fmaf(p, t, -0.053684855f);
+        p = fmaf(p, t, 0.12856221f);
+        p = fmaf(p, t, 0.09991333f);
+        p = fmaf(p, t, 0.12075398f);
+        q = fmaf(p, t, 0.11962929f) * t * e;
     } else {
-        e = expf(-0.5f * z * z);
-        return normcdff(z);
+        const float y = fminf(fabsf(z), 20.0f), sq = y * y;     // exp(-200) = 0 in fp32
+        e = ex2_scaled(sq, -0.72134751f, -9.6298151e-9f);
+        e = fmaf(e, fmaf(y, y, -sq) * -0.5f, e);                // the square's own rounding
+        const float t = rcp(fmaf(y, 0.35f, 1.0f));
+        float p = fmaf(t, -0.029145656f, 0.14397046f);
+        p = fmaf(p, t, -0.25571191f);
+        p = fmaf(p, t, 0.15917169f);
+        p = fmaf(p, t, -0.023108279f);
+        p = fmaf(p, t, 0.1055074f);
+        p = fmaf(p, t, 0.11983301f);
+        p = fmaf(p, t, 0.13986185f);
+        q = fmaf(p, t, 0.13962141f) * t * e;
     }
+    return z > 0.0f ? 1.0f - q : q;
 }
 
 // z -> act(z)
@@ -470,13 +480,18 @@ __global__ void __launch_bounds__(kThreads) k_norm_stats(const __grid_constant__
     });
 }
 
+// Lanes per group where a CTA adds up the tiles' sums.
+__host__ __device__ inline int merge_lanes(int groups) {
+    int L = 32;
+    while (L > 4 && kThreads / L < groups) L /= 2;
+    return L;
+}
+
 // f(g, lane, lanes) for the block's groups, several lanes of a warp to a group: all 32 for few groups, at least 4 for
 // many; all threads take part, those beyond the last group with group g1 and `valid` false.
 template <typename F>
 __device__ __forceinline__ void for_merges(const Block& b, F f) {
-    const int groups = b.g1 - b.g0 + 1;
-    int L = 32;
-    while (L > 4 && kThreads / L < groups) L /= 2;
+    const int L = merge_lanes(b.g1 - b.g0 + 1);
     for (int base = b.g0; base <= b.g1; base += kThreads / L) {
         const int g = base + threadIdx.x / L;
         f(min(g, b.g1), g <= b.g1, threadIdx.x % L, L);
@@ -856,8 +871,10 @@ void shape(NormArgs& a, int V, int chunk, int ctas) {
     while (a.glanes < 32 && a.glanes < std::min(a.width, a.nv * V)) a.glanes *= 2;
     a.magic = (uint32_t)((((uint64_t)1 << 32) + a.width - 1) / a.width);
     // tokens per tile, a multiple of the row lanes: kRowsPerThread a thread; less where that leaves SMs without CTAs, but
-    // not for more than kMaxTiles tiles, whose sums every CTA of the second pass adds up
-    const int64_t tiles = std::min<int64_t>(kMaxTiles, std::max(1, ctas / a.blocks));
+    // not for so many tiles that adding up their sums, which every CTA of the second pass does, takes long
+    const int groups = std::min(a.G, (a.nv * V + a.width - 2) / a.width + 1);
+    const int64_t most = std::max<int64_t>(kTilesPerLane * merge_lanes(groups), kMinTiles);
+    const int64_t tiles = std::min(most, (int64_t)std::max(1, ctas / a.blocks));
     a.R = (uint32_t)(a.rl * std::min<int64_t>(kRowsPerThread, cdiv(cdiv(a.N, tiles), a.rl)));
     a.slots = (uint32_t)(a.N / a.R + a.B);
 }
