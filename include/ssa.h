@@ -333,7 +333,8 @@ typedef struct {
 /*
  * Axis (0, 1, 2) and angular frequency of every rotated pair, as ssa_rotary uses them. Host only: needs
  * no device. axis: int32 [dim/2], freq: double [dim/2] (either may be NULL).
- * Errors: SSA_ERR_INVALID_ARG, SSA_ERR_UNSUPPORTED (head_dim outside the supported set).
+ * Errors: SSA_ERR_INVALID_ARG (also for a scaling that makes a frequency infinite), SSA_ERR_UNSUPPORTED (head_dim
+ * outside the supported set).
  */
 SSA_API ssa_status_t ssa_rotary_frequencies(const ssa_rotary_t* rotary, int32_t head_dim, int32_t* axis,
                                             double* freq);

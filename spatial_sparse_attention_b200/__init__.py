@@ -78,6 +78,7 @@ class Options(ctypes.Structure):
                 ("select_share", ctypes.c_int32)]
 
 
+_HERE_AND_NOW = contextlib.nullcontext()
 _ACTIVATION = {None: 0, "none": 0, "silu": 1, "gelu": 2}
 _LAYOUT = {"interleaved": 0, "half": 1}
 _SCALING = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -217,14 +218,22 @@ def _heads(t: Optional[torch.Tensor], plan: "Plan", like: torch.Tensor):
     contiguous), or NULL."""
     if t is None:
         return None
-    if t.device != plan.device or t.dtype != like.dtype:
+    if t.dtype is not like.dtype or t.device != plan.device:
         raise ValueError("expected tensors of one type on the plan's device")
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     if len(shape) != 3 or shape[0] != plan.N or shape[2] != like.shape[2]:
         raise ValueError("expected [N, heads, D]")
-    if stride[2] != 1:
+    token, head, channel = t.stride()
+    if channel != 1:
         raise ValueError("the channels of a head must be contiguous")
-    return _Heads(t.data_ptr(), stride[0], stride[1], shape[1])
+    return _Heads(t.data_ptr(), token, head, shape[1])
+
+
+def _new_heads(like: torch.Tensor):
+    """A new contiguous [N, heads, D] tensor and its view."""
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    _, heads, D = t.shape
+    return t, _Heads(t.data_ptr(), heads * D, D, heads)
 
 
 class _Rows(ctypes.Structure):
@@ -451,7 +460,7 @@ class Plan:
     def _on_stream(self):
         """Context in which results are allocated: on the plan's stream, so that their memory is
         ordered with the kernels that write it."""
-        return contextlib.nullcontext() if self.stream is None else torch.cuda.stream(self.stream)
+        return _HERE_AND_NOW if self.stream is None else torch.cuda.stream(self.stream)
 
     def _stream_of(self) -> int:
         if self.stream is not None:
@@ -469,12 +478,13 @@ class Plan:
         D = q.shape[2]
         gq = _weights(q_gamma, D, q, "q_gamma")
         gk = None if k is None else _weights(k_gamma, D, q, "k_gamma")
-        with self._on_stream():
-            if q_out is None:
-                q_out = _like(q)
-            if k_out is None and k is not None:
-                k_out = _like(k)
         oq, ok = _heads(q_out, self, q), _heads(k_out, self, q)
+        if q_out is None or (k_out is None and k is not None):
+            with self._on_stream():
+                if q_out is None:
+                    q_out, oq = _new_heads(q)
+                if k_out is None and k is not None:
+                    k_out, ok = _new_heads(k)
         _check(lib.ssa_rotary(self._h, ctypes.addressof(hq), _ref(hk), gq, gk, eps,
                               ctypes.addressof(rotary), D, _DTYPE.get(q.dtype, -1), ctypes.addressof(oq),
                               _ref(ok), self._stream_of()), "ssa_rotary")
@@ -495,16 +505,16 @@ class Plan:
         gk = _weights(k_gamma, D, dq_out, "k_gamma") if keys else None
         hq = _heads(q, self, dq_out) if norm else None
         hk = _heads(k, self, dq_out) if norm and keys else None
+        oq, ok = _heads(dq, self, dq_out), _heads(dk, self, dq_out)
         wq = wk = None
         with self._on_stream():
             if dq is None:
-                dq = _like(dq_out)
+                dq, oq = _new_heads(dq_out)
             if dk is None and keys:
-                dk = _like(dk_out)
+                dk, ok = _new_heads(dk_out)
             if norm:
                 wq = torch.empty_like(q_gamma)
                 wk = torch.empty_like(k_gamma) if keys and k_gamma is not None else None
-        oq, ok = _heads(dq, self, dq_out), _heads(dk, self, dq_out)
         _check(lib.ssa_rotary_backward(self._h, ctypes.addressof(gq_), _ref(gk_), _ref(hq), _ref(hk), gq,
                                        gk, eps, ctypes.addressof(rotary), D, _DTYPE.get(dq_out.dtype, -1),
                                        ctypes.addressof(oq), _ref(ok), _ptr(wq), _ptr(wk),

@@ -942,11 +942,14 @@ ssa_status_t run_norm(Plan* p, const Call& c, int32_t C, int32_t G, float eps, i
     a.chan_part = a.group_part + n_group;
     a.mean = c.mean;
     a.rstd = c.rstd;
+    const char* name = grad ? "group_norm_backward" : "group_norm";
+    ProfScope ps(name, st);
     const Launch l = {grad, act, A, p->device, st};
     const bool ok = dt == SSA_F32    ? launch_type<float>(a, l)
                     : dt == SSA_BF16 ? launch_type<__nv_bfloat16>(a, l)
                                      : launch_type<__half>(a, l);
     p->release(a.group_part, st, p->alloc_ctx);
+    trace_step(name, st);
     return ok && cudaGetLastError() == cudaSuccess ? SSA_OK : SSA_ERR_CUDA;
 }
 

@@ -667,6 +667,7 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
     double freq[kMaxPairs];
     a.pairs = rotary_frequencies(*rot, D, axis, freq);
     for (int i = 0; i < a.pairs; ++i) {
+        if (!std::isfinite(freq[i])) return SSA_ERR_INVALID_ARG;
         const long double turn = (long double)freq[i] * 0.15915494309189533576888376337251436L;   // 1 / (2 pi)
         const long double frac = turn - std::floor(turn);
         a.turns[i] = (uint64_t)(frac * 18446744073709551616.0L);   // 2^64
@@ -715,6 +716,8 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
         a.tile = tile_of(a.t[0].H + a.t[1].H);
     }
     const int64_t tiles = cdiv(N, a.tile);
+    const char* name = backward ? "rotary_backward" : "rotary";
+    ProfScope ps(name, st);
     ssa_status_t out = SSA_OK;
     if (!grad) {
         if (!launch_rows(a, (unsigned)tiles, dt, V, half, false, st)) out = SSA_ERR_CUDA;
@@ -738,6 +741,7 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
         }
     }
     if (out == SSA_OK && cudaGetLastError() != cudaSuccess) out = SSA_ERR_CUDA;
+    trace_step(name, st);
     return out;
 }
 
@@ -755,6 +759,8 @@ ssa_status_t ssa_rotary_frequencies(const ssa_rotary_t* rotary, int32_t head_dim
     int32_t ax[kMaxPairs];
     double f[kMaxPairs];
     const int n = rotary_frequencies(*rotary, head_dim, ax, f);
+    for (int i = 0; i < n; ++i)
+        if (!std::isfinite(f[i])) return SSA_ERR_INVALID_ARG;
     for (int i = 0; i < n; ++i) {
         if (axis) axis[i] = ax[i];
         if (freq) freq[i] = f[i];

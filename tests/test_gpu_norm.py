@@ -174,6 +174,20 @@ def test_longer_sequences(C, groups, dtype):
     check_backward(plan, cu, dy, x, groups, w, act="silu")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C,groups", [(100, 4), (36, 2), (1658, 1), (211, 1), (2045, 5), (12, 12)])
+def test_rows_of_every_alignment(dtype, C, groups):
+    """Rows that start at multiples of 2, 4, 8 and 16 bytes, with a part of a vector at their ends."""
+    plan, cu = plan_of((17, 300, 2, 2000))
+    buf = torch.full((2319 + 1, C), 7.0, dtype=ref.DTYPES[dtype], device="cuda")
+    x, dy, w = features(2319, C, dtype, C).cuda(), features(2319, C, dtype, 2).cuda(), weights(C, 3)
+    check_forward(plan, cu, x, groups, w, act="gelu", out=buf[:-1])
+    assert (buf[-1] == 7).all()
+    buf.fill_(7.0)
+    check_backward(plan, cu, dy, x, groups, w, act="gelu", dx=buf[1:])
+    assert (buf[0] == 7).all()
+
+
 def test_wide_rows():
     plan, cu = plan_of((3, 2))
     for C, groups in ((65536, 1), (65535, 3), (65536, 65536)):
@@ -370,6 +384,24 @@ def test_captured_and_replayed(C, groups, seqs):
 
 
 # ---- with the other operators ----------------------------------------------------------------------
+
+def test_profiled_by_name():
+    plan, cu = plan_of((300,))
+    x = features(300, 64, "f32", 1).cuda()
+    ssa.profile_reset()
+    ssa.profile_enable(True)
+    try:
+        _, m, r = plan.group_norm(x, 8, return_stats=True)
+        plan.group_norm_backward(x, x, m, r, 8)
+        plan.rotary(x.view(300, 2, 32))
+        plan.rotary_backward(x.view(300, 2, 32))
+        got = ssa.profile_read()
+    finally:
+        ssa.profile_enable(False)
+        ssa.profile_reset()
+    for name in ("group_norm", "group_norm_backward", "rotary", "rotary_backward"):
+        assert got[name][1] == 1 and got[name][0] > 0
+
 
 def test_layer_from_features_to_attention_and_back():
     """norm -> activation -> projection -> rotary positions -> attention, forward and gradients, against the same

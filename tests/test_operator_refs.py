@@ -100,6 +100,7 @@ def test_frequencies_refuse(field, value):
 
 @pytest.mark.parametrize("opt", [dict(scaling="linear", scale=0.0), dict(scaling="ntk", scale=-1.0),
                                  dict(scaling="linear", scale=float("inf")),
+                                 dict(scaling="linear", scale=5e-324), dict(scaling="ntk", scale=5e-324),
                                  dict(scaling="yarn", scale=2.0, extent=0.0),
                                  dict(scaling="yarn", scale=2.0, extent=64.0, beta_slow=8.0, beta_fast=8.0),
                                  dict(scaling="yarn", scale=2.0, extent=64.0, beta_slow=-1.0)])
