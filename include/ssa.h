@@ -365,8 +365,8 @@ SSA_API ssa_status_t ssa_rotary(ssa_plan_t plan, const ssa_heads_t* q, const ssa
  * and, when the weights are set, dq_gamma, dk_gamma (device fp32 [head_dim] each, sums over all tokens and
  * heads; written, not added to). q and k are the forward's inputs and are read only when the weights are
  * set (else they may be NULL). k-side pointers all NULL: queries only. dq and dk may be dq_out and dk_out
- * themselves (or q and k); otherwise as the outputs of ssa_rotary. Fixed summation order: equal inputs give
- * equal bits. Partial sums go to a buffer that is allocated and freed stream-ordered through the
+ * themselves (or q and k); otherwise as the outputs of ssa_rotary. Fixed summation order: equal inputs, alignment
+ * included, give equal bits. Partial sums go to a buffer that is allocated and freed stream-ordered through the
  * allocator. Otherwise as ssa_rotary; also SSA_ERR_ALLOC.
  */
 SSA_API ssa_status_t ssa_rotary_backward(ssa_plan_t plan, const ssa_heads_t* dq_out,
@@ -396,8 +396,8 @@ typedef enum { SSA_ACT_NONE = 0, SSA_ACT_SILU = 1, SSA_ACT_GELU = 2 } ssa_activa
  *   y: output; may be x itself (same pointer and stride), otherwise shares no memory with x.
  *   mean, rstd: outputs, device fp32 [B, groups], both or (NULL) neither; 0 for a sequence without tokens.
  * fp32 arithmetic, statistics merged in fp64, one rounding to the type at the end; the variance comes from
- * deviations, not from a difference of large sums. Fixed summation order: equal inputs give equal bits. Strides
- * >= 0 (y: >= channels). Queues work on `stream` and returns without waiting; partial sums go to a buffer that
+ * deviations, not from a difference of large sums. Fixed summation order: equal inputs, alignment included, give equal
+ * bits. Strides >= 0 (y: >= channels). Queues work on `stream` and returns without waiting; partial sums go to a buffer that
  * is allocated and freed stream-ordered through the allocator. Runs on the plan's device.
  * Errors: SSA_ERR_INVALID_ARG, SSA_ERR_UNSUPPORTED (more than 65536 channels), SSA_ERR_ALLOC, SSA_ERR_CUDA.
  */

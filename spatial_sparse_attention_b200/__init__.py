@@ -538,7 +538,8 @@ class Plan:
             if out is None:
                 out = _like(x)
             if return_stats:
-                mean, rstd = self._f32.new_empty((2, self.batch, groups)).unbind(0)
+                mean = self._f32.new_empty((self.batch, groups))
+                rstd = torch.empty_like(mean)
         vy = _rows(out, self, x)
         _check(lib.ssa_group_norm(self._h, ctypes.addressof(vx), C, groups, wg, wb, eps, act,
                                   _DTYPE.get(x.dtype, -1), ctypes.addressof(vy), _ptr(mean), _ptr(rstd),
@@ -557,7 +558,8 @@ class Plan:
         with self._on_stream():
             if dx is None:
                 dx = _like(x)
-            dgamma, dbeta = self._f32.new_empty((2, C)).unbind(0)
+            dgamma = self._f32.new_empty(C) if gamma is None else torch.empty_like(gamma)
+            dbeta = torch.empty_like(dgamma)
         vo = _rows(dx, self, x)
         _check(lib.ssa_group_norm_backward(self._h, ctypes.addressof(vd), ctypes.addressof(vx), m, r, C, groups,
                                            wg, wb, act, _DTYPE.get(x.dtype, -1), ctypes.addressof(vo),

@@ -27,6 +27,7 @@ constexpr int kMaxTile = 32;      // tokens per CTA tile, at most one per lane
 constexpr int kMaxPairs = 64;     // head_dim <= 128
 constexpr int kLane = 32;         // bytes of a row per lane
 constexpr int kStages = 3;        // rows per lane in flight or in use, forward
+constexpr int kStagedBelow = 2;   // half layout: loads of at most this many elements are staged
 constexpr int kGradStages = 3;    // gradient (two rows each)
 
 struct RowsArg {
@@ -102,39 +103,68 @@ __device__ __forceinline__ void turn_cos_sin(int32_t coord, uint64_t turns, floa
     if (q & 2) s = -s;
 }
 
-// A lane's places in the ring of rows in flight: chunk i of stage `stage`, neighbouring lanes side by side.
-template <typename CUT>
-__device__ __forceinline__ typename CUT::C* ring_at(char* ring, int stage, int i) {
-    return (typename CUT::C*)(ring + (stage * CUT::N + i) * (kThreads * sizeof(typename CUT::C))) + threadIdx.x;
-}
+// Bytes of the rows that a CTA has in one stage. Staged rows are 16 bytes apart, so that the same element of a warp's
+// rows (of up to 16) lies in different banks.
+constexpr int kRowPad = 16;
+__host__ __device__ constexpr int stage_bytes(bool staged) { return kThreads * kLane + (staged ? kWarps * 16 * kRowPad : 0); }
 
-template <typename CUT, typename T>
-__device__ __forceinline__ void fetch_row(char* ring, int stage, const T* row, const int (&off)[CUT::N]) {
-#pragma unroll
-    for (int i = 0; i < CUT::N; ++i) cp_async<sizeof(typename CUT::C)>(ring_at<CUT>(ring, stage, i), row + off[i]);
-}
-
-template <typename CUT, typename T>
-__device__ __forceinline__ void read_row(char* ring, int stage, float (&e)[CUT::E]) {
-#pragma unroll
-    for (int i = 0; i < CUT::N; ++i) {
-        float v[CUT::V];
-        Vec<T, CUT::V>::unpack(*ring_at<CUT>(ring, stage, i), v);
-#pragma unroll
-        for (int j = 0; j < CUT::V; ++j) e[CUT::reg(i, j)] = v[j];
+// A lane group's row in flight. Direct: a lane's loads lie in places of its own, neighbouring lanes side by side.
+// STAGED (the half layout where the two sides of the pairs do not start at a vector): the row lies in its natural
+// order, fetched and stored in 16-byte chunks, and the lanes pick their pairs' elements out of it and put them back.
+template <typename T, typename CUT, bool STAGED>
+struct Slot {
+    using C = typename CUT::C;
+    char* at;       // direct: this lane's first chunk; staged: the row
+    int l, G;
+    __device__ __forceinline__ Slot(char* ring, int stage, int sub, int l_, int G_) : l(l_), G(G_) {
+        char* const base = ring + stage * stage_bytes(STAGED);
+        at = STAGED ? base + (threadIdx.x >> 5) * (stage_bytes(true) / kWarps) + sub * (G * kLane + kRowPad)
+                    : base + threadIdx.x * sizeof(C);
     }
-}
-
-template <typename CUT, typename T>
-__device__ __forceinline__ void store_row(T* row, const int (&off)[CUT::N], const float (&e)[CUT::E]) {
+    __device__ __forceinline__ C* place(int i) const { return (C*)(at + i * (kThreads * sizeof(C))); }
+    __device__ __forceinline__ int chunk(int i) const { return (i * G + l) * 16; }
+    __device__ __forceinline__ void fetch(const T* row, const int (&off)[CUT::N]) const {
+        if constexpr (STAGED) {
 #pragma unroll
-    for (int i = 0; i < CUT::N; ++i) {
-        float v[CUT::V];
+            for (int i = 0; i < kLane / 16; ++i) cp_async<16>(at + chunk(i), (const char*)row + chunk(i));
+        } else {
 #pragma unroll
-        for (int j = 0; j < CUT::V; ++j) v[j] = e[CUT::reg(i, j)];
-        *reinterpret_cast<typename CUT::C*>(row + off[i]) = Vec<T, CUT::V>::pack(v);
+            for (int i = 0; i < CUT::N; ++i) cp_async<sizeof(C)>(place(i), row + off[i]);
+        }
     }
-}
+    // after the copies have landed (staged: and a __syncwarp)
+    __device__ __forceinline__ void read(const int (&off)[CUT::N], float (&e)[CUT::E]) const {
+#pragma unroll
+        for (int i = 0; i < CUT::N; ++i) {
+            float v[CUT::V];
+            if constexpr (STAGED) v[0] = Elem<T>::to_f(((const T*)at)[off[i]]);
+            else Vec<T, CUT::V>::unpack(*place(i), v);
+#pragma unroll
+            for (int j = 0; j < CUT::V; ++j) e[CUT::reg(i, j)] = v[j];
+        }
+    }
+    // staged: the lane's elements back into the row; then, after a __syncwarp, `write` stores the row
+    __device__ __forceinline__ void put_back(const int (&off)[CUT::N], const float (&e)[CUT::E]) const {
+        if constexpr (STAGED) {
+#pragma unroll
+            for (int i = 0; i < CUT::N; ++i) ((T*)at)[off[i]] = Elem<T>::from_f(e[i]);
+        }
+    }
+    __device__ __forceinline__ void write(T* row, const int (&off)[CUT::N], const float (&e)[CUT::E]) const {
+        if constexpr (STAGED) {
+#pragma unroll
+            for (int i = 0; i < kLane / 16; ++i) *(uint4*)((char*)row + chunk(i)) = *(const uint4*)(at + chunk(i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < CUT::N; ++i) {
+                float v[CUT::V];
+#pragma unroll
+                for (int j = 0; j < CUT::V; ++j) v[j] = e[CUT::reg(i, j)];
+                *reinterpret_cast<C*>(row + off[i]) = Vec<T, CUT::V>::pack(v);
+            }
+        }
+    }
+};
 
 // A lane's weights, from a table in register order: item `it` at it * 2P.
 template <typename CUT>
@@ -150,8 +180,9 @@ __device__ __forceinline__ void read_gamma(const float* gamma, int l, int G, flo
                 g[m * W + j] = v.x; g[m * W + j + 1] = v.y; g[m * W + j + 2] = v.z; g[m * W + j + 3] = v.w;
             }
         } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j) g[m * W + j] = at[j];
+            const float2 v = *reinterpret_cast<const float2*>(at);
+            g[m * W] = v.x;
+            g[m * W + 1] = v.y;
         }
     }
 }
@@ -310,12 +341,12 @@ struct Cursor {
 
 // out = rotate(normalise(x)), or the rotation back (sgn = -1, no weights). One tile of tokens per CTA, the
 // queries' heads then the keys'; warps take row after row.
-template <typename T, int V, bool HALF, bool NORM, int LANES>
+template <typename T, int V, bool HALF, bool NORM, int LANES, bool STAGED>
 __global__ void __launch_bounds__(kThreads, 4) k_rotary(const __grid_constant__ RotArgs a) {
     using CUT = Cut<T, V, HALF>;
     constexpr int E = CUT::E;
     extern __shared__ __align__(16) char smem[];    // ring, tables, weights
-    float* cs = (float*)(smem + kStages * kLane * kThreads);
+    float* cs = (float*)(smem + kStages * stage_bytes(STAGED));
     float* sn = cs + a.tile * tab_stride(a.D);
     float* gamma = sn + a.tile * tab_stride(a.D);
     const int64_t tok0 = (int64_t)blockIdx.x * a.tile;
@@ -335,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_rotary(const __grid_constant__ 
         if (ahead.r < nrow) {
             const bool second = ahead.h >= H0;
             const RowsArg& t = a.t[second];
-            fetch_row<CUT, T>(smem, stage,
-                              (const T*)t.x + (tok0 + ahead.t) * t.x_ts + (ahead.h - (second ? H0 : 0)) * t.x_hs, off);
+            Slot<T, CUT, STAGED>(smem, stage, sub, l, G)
+                .fetch((const T*)t.x + (tok0 + ahead.t) * t.x_ts + (ahead.h - (second ? H0 : 0)) * t.x_hs, off);
         }
         cp_commit();
         ahead.advance(step, dt, dh, H);
@@ -355,8 +386,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_rotary(const __grid_constant__ 
         fetch((stage + kStages - 1) % kStages);
         cp_wait<kStages - 1>();
         const bool mine = at.r < nrow, second = at.h >= H0;
+        const Slot<T, CUT, STAGED> slot(smem, stage, sub, l, G);
         float e[E];
-        if (mine) read_row<CUT, T>(smem, stage, e);
+        if (STAGED) __syncwarp();
+        if (mine) slot.read(off, e);
         if constexpr (NORM) {
             float ss[1] = {0.0f}, odd = 0.0f;
             if (mine) {
@@ -377,10 +410,14 @@ __global__ void __launch_bounds__(kThreads, 4) k_rotary(const __grid_constant__ 
             }
         }
         if (mine) {
-            const RowsArg& t = a.t[second];
             const int tab = at.t * tab_stride(a.D);
             turn_row<CUT>(e, cs + tab, sn + tab, l, G, a.pairs);
-            store_row<CUT, T>((T*)t.out + (tok0 + at.t) * t.o_ts + (at.h - (second ? H0 : 0)) * t.o_hs, off, e);
+            slot.put_back(off, e);
+        }
+        if (STAGED) __syncwarp();
+        if (mine) {
+            const RowsArg& t = a.t[second];
+            slot.write((T*)t.out + (tok0 + at.t) * t.o_ts + (at.h - (second ? H0 : 0)) * t.o_hs, off, e);
         }
         at.advance(step, dt, dh, H);
         stage = (stage + 1) % kStages;
@@ -390,13 +427,13 @@ __global__ void __launch_bounds__(kThreads, 4) k_rotary(const __grid_constant__ 
 // The gradient with weights. Persistent: a CTA walks tiles of its tensor, its loads running ahead into the
 // next tile, and keeps the weights' sums of its lanes' channels in registers; it adds them up over its rows in a
 // fixed order at the end.
-template <typename T, int V, bool HALF, int LANES>
+template <typename T, int V, bool HALF, int LANES, bool STAGED>
 __global__ void __launch_bounds__(kThreads, 2) k_rotary_grad(const __grid_constant__ RotArgs a) {
     using CUT = Cut<T, V, HALF>;
     constexpr int E = CUT::E, S = kGradStages;
     extern __shared__ __align__(16) char smem[];
-    char* const ring_g = smem + S * kLane * kThreads;
-    float* cs = (float*)(smem + 2 * S * kLane * kThreads);
+    char* const ring_g = smem + S * stage_bytes(STAGED);
+    float* cs = (float*)(smem + 2 * S * stage_bytes(STAGED));
     float* sn = cs + a.tile * tab_stride(a.D);
     float* gamma = sn + a.tile * tab_stride(a.D);
     const int which = blockIdx.x < a.ctas0 ? 0 : 1;
@@ -422,8 +459,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_rotary_grad(const __grid_consta
         if (ftok < a.N) {
             if (fbase == 0) frow = (int)min((int64_t)t.tile, a.N - ftok) * H;
             if (ahead.r < frow && sub < rpw) {
-                fetch_row<CUT, T>(smem, stage, (const T*)t.x + (ftok + ahead.t) * t.x_ts + ahead.h * t.x_hs, off);
-                fetch_row<CUT, T>(ring_g, stage, (const T*)t.g + (ftok + ahead.t) * t.g_ts + ahead.h * t.g_hs, off);
+                Slot<T, CUT, STAGED>(smem, stage, sub, l, G)
+                    .fetch((const T*)t.x + (ftok + ahead.t) * t.x_ts + ahead.h * t.x_hs, off);
+                Slot<T, CUT, STAGED>(ring_g, stage, sub, l, G)
+                    .fetch((const T*)t.g + (ftok + ahead.t) * t.g_ts + ahead.h * t.g_hs, off);
             }
             ahead.advance(step, dt, dh, H);
             fbase += step;
@@ -455,9 +494,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_rotary_grad(const __grid_consta
             cp_wait<S - 1>();
             const bool mine = at.r < nrow && sub < rpw;
             float e[E], d[E], sums[2] = {0.0f, 0.0f};   // sum x^2, sum du gamma x
+            const Slot<T, CUT, STAGED> slot(ring_g, stage, sub, l, G);
+            if (STAGED) __syncwarp();
             if (mine) {
-                read_row<CUT, T>(smem, stage, e);
-                read_row<CUT, T>(ring_g, stage, d);
+                Slot<T, CUT, STAGED>(smem, stage, sub, l, G).read(off, e);
+                slot.read(off, d);
                 const int tab = at.t * tab_stride(a.D);
                 turn_row<CUT>(d, cs + tab, sn + tab, l, G, a.pairs);
                 float odd0 = 0.0f, odd1 = 0.0f;
@@ -484,8 +525,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_rotary_grad(const __grid_consta
                     fma2(d[i], d[i + 1], n0, n1, dot, dot, d[i], d[i + 1]);
                     mul2(d[i], d[i + 1], d[i], d[i + 1], inv, inv);
                 }
-                store_row<CUT, T>(out + at.t * t.o_ts + at.h * t.o_hs, off, d);
+                slot.put_back(off, d);
             }
+            if (STAGED) __syncwarp();
+            if (mine) slot.write(out + at.t * t.o_ts + at.h * t.o_hs, off, d);
             at.advance(step, dt, dh, H);
             stage = (stage + 1) % S;
         }
@@ -579,37 +622,43 @@ bool launch_one(const RotArgs& a, unsigned grid, size_t smem, cudaStream_t st) {
     return true;
 }
 
-template <typename T, int V, bool HALF, int LANES>
+template <typename T, int V, bool HALF, int LANES, bool STAGED>
 bool launch_lanes(const RotArgs& a, unsigned grid, bool grad, cudaStream_t st) {
-    const size_t ring = (size_t)kLane * kThreads, tables = sizeof(float) * 2 * ((size_t)a.tile * tab_stride(a.D) + a.D);
-    if (grad) return launch_one<k_rotary_grad<T, V, HALF, LANES>>(a, grid, 2 * kGradStages * ring + tables, st);
-    if (a.t[0].gamma) return launch_one<k_rotary<T, V, HALF, true, LANES>>(a, grid, kStages * ring + tables, st);
-    return launch_one<k_rotary<T, V, HALF, false, LANES>>(a, grid, kStages * ring + tables, st);
+    const size_t ring = stage_bytes(STAGED), tables = sizeof(float) * 2 * ((size_t)a.tile * tab_stride(a.D) + a.D);
+    if (grad) return launch_one<k_rotary_grad<T, V, HALF, LANES, STAGED>>(a, grid, 2 * kGradStages * ring + tables, st);
+    if (a.t[0].gamma) return launch_one<k_rotary<T, V, HALF, true, LANES, STAGED>>(a, grid, kStages * ring + tables, st);
+    return launch_one<k_rotary<T, V, HALF, false, LANES, STAGED>>(a, grid, kStages * ring + tables, st);
 }
 
-// Loads of 16 and 8 bytes with the lanes per row known at compile time (a shuffle tree and offsets without
-// branches: 350 against 437 us for the gradient of 80,000 tokens x 44 heads x 96); rows aligned to less
-// with them at run time.
-template <typename T, int V, bool HALF>
+// Full vectors (half layout: halves of one too) with the lanes per row known at compile time (a shuffle tree and offsets without branches: 350
+// against 437 us for the gradient of 80,000 tokens x 44 heads x 96); rows aligned to less with them at run time.
+template <typename T, int V, bool HALF, bool STAGED>
 bool launch_cut(const RotArgs& a, unsigned grid, bool grad, cudaStream_t st) {
     constexpr int D32 = 32 * (int)sizeof(T) / kLane;    // lanes of 32 channels
-    if constexpr (V * sizeof(T) >= 8) {
-        if (a.D == 32) return launch_lanes<T, V, HALF, D32>(a, grid, grad, st);
-        if (a.D == 64) return launch_lanes<T, V, HALF, 2 * D32>(a, grid, grad, st);
-        if (a.D == 96) return launch_lanes<T, V, HALF, 3 * D32>(a, grid, grad, st);
-        return launch_lanes<T, V, HALF, 4 * D32>(a, grid, grad, st);
+    if constexpr (STAGED || V * sizeof(T) == 16 || (HALF && V * sizeof(T) == 8)) {
+        if (a.D == 32) return launch_lanes<T, V, HALF, D32, STAGED>(a, grid, grad, st);
+        if (a.D == 64) return launch_lanes<T, V, HALF, 2 * D32, STAGED>(a, grid, grad, st);
+        if (a.D == 96) return launch_lanes<T, V, HALF, 3 * D32, STAGED>(a, grid, grad, st);
+        return launch_lanes<T, V, HALF, 4 * D32, STAGED>(a, grid, grad, st);
     } else {
-        return launch_lanes<T, V, HALF, 0>(a, grid, grad, st);
+        return launch_lanes<T, V, HALF, 0, STAGED>(a, grid, grad, st);
     }
 }
 
 template <typename T, int V>
 bool launch_layout(const RotArgs& a, unsigned grid, bool half, bool grad, cudaStream_t st) {
     note_launch();
-    return half ? launch_cut<T, V, true>(a, grid, grad, st) : launch_cut<T, V, false>(a, grid, grad, st);
+    return half ? launch_cut<T, V, true, false>(a, grid, grad, st) : launch_cut<T, V, false, false>(a, grid, grad, st);
 }
 
+// V: elements per load; 0: staged.
 bool launch_rows(const RotArgs& a, unsigned grid, ssa_dtype_t dt, int V, bool half, bool grad, cudaStream_t st) {
+    if (V == 0) {
+        note_launch();
+        if (dt == SSA_F32) return launch_cut<float, 1, true, true>(a, grid, grad, st);
+        if (dt == SSA_BF16) return launch_cut<__nv_bfloat16, 1, true, true>(a, grid, grad, st);
+        return launch_cut<__half, 1, true, true>(a, grid, grad, st);
+    }
     if (dt == SSA_F32) {
         if (V >= 4) return launch_layout<float, 4>(a, grid, half, grad, st);
         if (V == 2) return launch_layout<float, 2>(a, grid, half, grad, st);
@@ -674,9 +723,8 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
         a.axis[i] = (uint8_t)axis[i];
     }
     const bool half = rot->layout == SSA_ROTARY_HALF, grad = backward && norm;
-    int V = dt == SSA_F32 ? 4 : 8;
-    // in the half layout a vector holds one side of V pairs, so 2V has to divide the rotated width
-    while (half && V > 1 && 2 * a.pairs % (2 * V)) V >>= 1;
+    const int full = dt == SSA_F32 ? 4 : 8;
+    int V = full;
     for (int i = 0; i < nt; ++i) {
         V = view_vector(*c.out[i], N, es, V);
         for (int j = 0; j < 2; ++j)
@@ -689,6 +737,11 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
                     x->token_stride, x->head_stride, g->token_stride, g->head_stride,
                     c.out[i]->token_stride, c.out[i]->head_stride, x->heads, 0};
     }
+    // in the half layout a vector holds one side of V pairs, so 2V has to divide the rotated width; where that leaves short
+    // loads of aligned rows, the rows go through shared memory whole
+    int side = V;
+    while (half && side > 1 && a.pairs % side) side >>= 1;
+    V = V == full && side <= kStagedBelow ? (side < full ? 0 : V) : side;
     a.coords = p->coords;
     a.N = N;
     a.D = D;

@@ -282,6 +282,35 @@ def test_in_place(layout, norm):
             assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("D,dim", [(32, 6), (64, 54), (96, 26), (96, 88), (128, 100), (128, 2)])
+def test_half_layout_off_the_vectors(dtype, D, dim):
+    """Sides of pairs that do not start at 16 bytes: aligned rows, rows that are not, in place, other rows' memory."""
+    n, h = 333, 5
+    plan, c = one_plan(n)
+    opt = dict(layout="half", dim=dim, scaling="ntk", scale=2.0)
+    fused = rows((n, 3 * h, D), dtype, 1).cuda()
+    q, k = fused[:, :h], fused[:, h:2 * h - 2]
+    odd = torch.zeros(n * h * D + 1, dtype=fused.dtype, device="cuda")[1:].view(n, h, D)
+    odd.copy_(q)
+    for w in (weights(D, 5), (None, None)):
+        check_forward(plan, c, q, k, opt, w)
+        check_forward(plan, c, odd, k, opt, w)
+        check_backward(plan, c, k[:, :1].expand(n, h, D), q[:, :3], q, k, opt, w)
+        r, wd = ssa.Rotary(**opt), [None if v is None else v.cuda() for v in w]
+        want = plan.rotary(q, k, r, *wd)
+        buf = fused.clone()
+        got = plan.rotary(buf[:, :h], buf[:, h:2 * h - 2], r, *wd, q_out=buf[:, :h], k_out=buf[:, h:2 * h - 2])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(buf[:, 2 * h - 2:], fused[:, 2 * h - 2:])
+        grads = plan.rotary_backward(q, k, r, k[:, :1].expand(n, h, D), q[:, :3], *wd)
+        buf = fused.clone()
+        got = plan.rotary_backward(buf[:, :h], buf[:, h:2 * h - 2], r, k[:, :1].expand(n, h, D), q[:, :3], *wd,
+                                   dq=buf[:, :h], dk=buf[:, h:2 * h - 2])
+        assert all(torch.equal(a, b) for a, b in zip(got, grads))
+        assert torch.equal(buf[:, 2 * h - 2:], fused[:, 2 * h - 2:])
+
+
 def test_queries_only():
     plan, c = one_plan(33)
     q, k = rows((33, 3, 64), "f16", 1).cuda(), rows((33, 2, 64), "f16", 2).cuda()
