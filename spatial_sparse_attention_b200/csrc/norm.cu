@@ -21,6 +21,8 @@
 #include <cmath>
 #include <type_traits>
 
+#include <cooperative_groups.h>
+
 #include "views.cuh"
 
 namespace ssa {
@@ -39,6 +41,8 @@ constexpr int kMinTiles = 148;          // where that does not leave SMs without
 constexpr int kBlockBytes = 128;        // of a row that a column block's threads read together, at least
 constexpr int kStages = 8;              // rows per thread in flight or in use: forward, gradient
 constexpr int kGradStages = 6;
+constexpr int kKeptRows = 12;           // rows per thread and CTAs per SM of the one-launch forward: 198 KB of 227
+constexpr int kKeptCtas = 3;
 
 struct NormArgs {
     const void* x;
@@ -188,6 +192,13 @@ struct Rows {
             for (int i = 0; i < STAGES - 1; ++i) fetch(i);
         }
     }
+    // all rows at once, to be kept: count <= STAGES
+    __device__ __forceinline__ void start_kept() {
+        left = count;
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) fetch(i);
+        cp_wait<0>();
+    }
     // channels beyond the row come out as anything: nothing is made of them
     __device__ __forceinline__ void read(int stage, int k, float (&e)[V]) {
 #pragma unroll
@@ -199,8 +210,11 @@ struct Rows {
             if (N == 1 || i < chunks) raw[i] = *reinterpret_cast<const C*>(from + i * hop);
     }
     // row 0, which stays to be read (count > 0)
+    template <bool KEPT>
     __device__ __forceinline__ void peek(float (&e)[V]) {
-        if constexpr (kRing) {
+        if constexpr (KEPT) {
+            read(0, 0, e);
+        } else if constexpr (kRing) {
             cp_wait<STAGES - 2>();
             read(0, 0, e);
         } else {
@@ -211,10 +225,17 @@ struct Rows {
         }
     }
     // f(e) for every row, e[k] being its vector of array k; f may write over the row (in place)
-    template <typename F>
+    template <bool KEPT, typename F>
     __device__ __forceinline__ void each(F f) {
         float e[K][V];
-        if constexpr (kRing) {
+        if constexpr (KEPT) {
+#pragma unroll 4
+            for (int i = 0; i < count; ++i) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) read(i, k, e[k]);
+                f(e);
+            }
+        } else if constexpr (kRing) {
             for (int i = 0; i < count; i += STAGES) {
 #pragma unroll
                 for (int j = 0; j < STAGES; ++j) {
@@ -402,35 +423,27 @@ __device__ __forceinline__ void wait_for_last_launch() { asm volatile("griddepco
 
 // ---- forward -----------------------------------------------------------------------------------
 
-// Sums of the tile's segments: per group of the column block, mean and squared deviations.
-template <typename T, int A>
-__global__ void __launch_bounds__(kThreads) k_norm_stats(const __grid_constant__ NormArgs a) {
+template <typename T, int A, int STAGES>
+__device__ __forceinline__ Rows<T, A, 1, STAGES> norm_rows(const NormArgs& a, const Block& b, const Tile& tile, char* ring) {
+    return {{(const T*)a.x + (tile.t0 + b.lane) * a.x_ts + b.c0 + b.vec * A}, {a.rl * a.x_ts}, row_count(a, b, tile.n),
+            b.chunks<A>(), b.nvec * A, ring};
+}
+
+// Mean and squared deviations of a tile per group of the column block, from its rows.
+template <typename T, int A, bool KEPT, typename ROWS>
+__device__ __forceinline__ void sum_tile(const NormArgs& a, const Block& b, const Tile& tile, ROWS& rows, float2* red) {
     constexpr int V = Pieces<T, A>::V;
-    extern __shared__ __align__(16) char smem[];
-    float2* red = (float2*)smem;        // [rl][red_row], then the ring
-    let_next_launch_start();
-    const uint32_t slot = blockIdx.x / a.blocks;
-    const Block b(a, blockIdx.x - slot * a.blocks, V);
-    const Tile tile(a, slot);
-    const int s = tile.s, n = tile.n, row_c = red_row(a, V);
-    if (n == 0) {
-        if (tile.tiles == 0 && a.mean)      // a sequence without tokens
-            for (int g = b.g0 + threadIdx.x; g <= b.g1; g += kThreads) a.mean[(int64_t)s * a.G + g] = a.rstd[(int64_t)s * a.G + g] = 0.0f;
-        return;
-    }
-    Rows<T, A, 1, kStages> rows = {{(const T*)a.x + (tile.t0 + b.lane) * a.x_ts + b.c0 + b.vec * A}, {a.rl * a.x_ts},
-                                   row_count(a, b, n), b.chunks<A>(), b.nvec * A, smem + red_bytes(a, V)};
-    rows.start();
-    const int count = rows.count;
+    const int n = tile.n, row_c = red_row(a, V), count = rows.count;
+    const uint32_t slot = tile.slot;
     if (count) {
         float p[V], sum[V], sq[V];      // p: the first row, negated
-        rows.peek(p);
+        rows.template peek<KEPT>(p);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             p[j] = -p[j];
             sum[j] = sq[j] = 0.0f;
         }
-        rows.each([&](const float (&e)[1][V]) {
+        rows.template each<KEPT>([&](const float (&e)[1][V]) {
 #pragma unroll
             for (int j = 0; j < V; j += 2) {
                 float d0, d1;
@@ -478,6 +491,28 @@ __global__ void __launch_bounds__(kThreads) k_norm_stats(const __grid_constant__
                 make_float2(first + d, sq - n * sum * d);
         }
     });
+}
+
+// Sequences without tokens have one empty tile.
+__device__ __forceinline__ void write_empty(const NormArgs& a, const Block& b, const Tile& tile) {
+    if (tile.tiles == 0 && a.mean)
+        for (int g = b.g0 + threadIdx.x; g <= b.g1; g += kThreads)
+            a.mean[(int64_t)tile.s * a.G + g] = a.rstd[(int64_t)tile.s * a.G + g] = 0.0f;
+}
+
+template <typename T, int A>
+__global__ void __launch_bounds__(kThreads) k_norm_stats(const __grid_constant__ NormArgs a) {
+    constexpr int V = Pieces<T, A>::V;
+    extern __shared__ __align__(16) char smem[];
+    float2* red = (float2*)smem;        // [rl][red_row], then the ring
+    let_next_launch_start();
+    const uint32_t slot = blockIdx.x / a.blocks;
+    const Block b(a, blockIdx.x - slot * a.blocks, V);
+    const Tile tile(a, slot);
+    if (tile.n == 0) return write_empty(a, b, tile);
+    auto rows = norm_rows<T, A, kStages>(a, b, tile, smem + red_bytes(a, V));
+    rows.start();
+    sum_tile<T, A, false>(a, b, tile, rows, red);
 }
 
 // Lanes per group where a CTA adds up the tiles' sums.
@@ -535,22 +570,10 @@ __device__ __forceinline__ void merge_stats(const NormArgs& a, const Block& b, c
     });
 }
 
-template <typename T, int A, int ACT>
-__global__ void __launch_bounds__(kThreads, 4) k_norm_apply(const __grid_constant__ NormArgs a) {
+// The outputs of a tile, with the groups' mean and rstd in `stats`.
+template <typename T, int A, int ACT, bool KEPT, typename ROWS>
+__device__ __forceinline__ void apply_tile(const NormArgs& a, const Block& b, const Tile& tile, ROWS& rows, const float2* stats) {
     constexpr int V = Pieces<T, A>::V;
-    extern __shared__ __align__(16) char smem[];
-    float2* stats = (float2*)(smem + Rows<T, A, 1, kStages>::kBytes);     // the block's groups, after the ring
-    const uint32_t i = gridDim.x - 1 - blockIdx.x, slot = i / a.blocks;
-    const Block b(a, i - slot * a.blocks, V);
-    const Tile tile(a, slot);
-    if (tile.n == 0) return;
-    const int c0 = b.c0 + b.vec * A;
-    Rows<T, A, 1, kStages> rows = {{(const T*)a.x + (tile.t0 + b.lane) * a.x_ts + c0}, {a.rl * a.x_ts},
-                                   row_count(a, b, tile.n), b.chunks<A>(), b.nvec * A, smem};
-    rows.start();
-    wait_for_last_launch();
-    merge_stats(a, b, tile, V, stats);
-    __syncthreads();
     if (rows.count) {
         float mean[V], scale[V], beta[V];       // mean: negated
 #pragma unroll
@@ -562,8 +585,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_norm_apply(const __grid_constan
             beta[j] = a.beta ? a.beta[c] : 0.0f;
         }
         const int64_t out_step = a.rl * a.o_ts;
-        T* out = (T*)a.out + (tile.t0 + b.lane) * a.o_ts + c0;
-        rows.each([&](const float (&e)[1][V]) {
+        T* out = (T*)a.out + (tile.t0 + b.lane) * a.o_ts + b.c0 + b.vec * A;
+        rows.template each<KEPT>([&](const float (&e)[1][V]) {
             float z[V];
 #pragma unroll
             for (int j = 0; j < V; j += 2) {
@@ -576,6 +599,47 @@ __global__ void __launch_bounds__(kThreads, 4) k_norm_apply(const __grid_constan
             out += out_step;
         });
     }
+}
+
+template <typename T, int A, int ACT>
+__global__ void __launch_bounds__(kThreads, 4) k_norm_apply(const __grid_constant__ NormArgs a) {
+    constexpr int V = Pieces<T, A>::V;
+    extern __shared__ __align__(16) char smem[];
+    float2* stats = (float2*)(smem + Rows<T, A, 1, kStages>::kBytes);     // the block's groups, after the ring
+    const uint32_t i = gridDim.x - 1 - blockIdx.x, slot = i / a.blocks;
+    const Block b(a, i - slot * a.blocks, V);
+    const Tile tile(a, slot);
+    if (tile.n == 0) return;
+    auto rows = norm_rows<T, A, kStages>(a, b, tile, smem);
+    rows.start();
+    wait_for_last_launch();
+    merge_stats(a, b, tile, V, stats);
+    __syncthreads();
+    apply_tile<T, A, ACT, false>(a, b, tile, rows, stats);
+}
+
+// Both passes in one cooperative launch, where all rows fit in the shared memory of the CTAs that run at once: read once,
+// and the second pass waits for the grid instead of for a launch.
+template <typename T, int A, int ACT>
+__global__ void __launch_bounds__(kThreads, kKeptCtas) k_norm_kept(const __grid_constant__ NormArgs a) {
+    constexpr int V = Pieces<T, A>::V;
+    extern __shared__ __align__(16) char smem[];
+    float2* red = (float2*)(smem + Rows<T, A, 1, kKeptRows>::kBytes);     // then the block's groups
+    const uint32_t slot = blockIdx.x / a.blocks;
+    const Block b(a, blockIdx.x - slot * a.blocks, V);
+    const Tile tile(a, slot);
+    auto rows = norm_rows<T, A, kKeptRows>(a, b, tile, smem);
+    if (tile.n == 0) {
+        write_empty(a, b, tile);
+    } else {
+        rows.start_kept();
+        sum_tile<T, A, true>(a, b, tile, rows, red);
+    }
+    cooperative_groups::this_grid().sync();
+    if (tile.n == 0) return;
+    merge_stats(a, b, tile, V, red);
+    __syncthreads();
+    apply_tile<T, A, ACT, true>(a, b, tile, rows, red);
 }
 
 // ---- gradient ------------------------------------------------------------------------------------
@@ -644,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_grad_sums(const __grid_con
         float s0[V], s1[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) s0[j] = s1[j] = 0.0f;
-        rows.each([&](const float (&e)[2][V]) {
+        rows.template each<false>([&](const float (&e)[2][V]) {
             float xc[V], dz[V];
             row_grad<T, V, ACT>(ch, e, xc, dz);
 #pragma unroll
@@ -777,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_norm_grad_apply(const __grid_co
         }
         const int64_t out_step = a.rl * a.o_ts;
         T* out = (T*)a.out + (tile.t0 + b.lane) * a.o_ts + c0;
-        rows.each([&](const float (&e)[2][V]) {
+        rows.template each<false>([&](const float (&e)[2][V]) {
             float xc[V], dz[V];
             row_grad<T, V, ACT>(ch, e, xc, dz);
 #pragma unroll
@@ -799,6 +863,7 @@ using Kernel = std::integral_constant<void (*)(NormArgs), K>;
 struct Launch {
     bool grad;
     int act, A, device;     // A: elements per chunk
+    bool kept;              // the one-launch forward
     cudaStream_t st;
 };
 
@@ -807,29 +872,44 @@ bool launch_act(const NormArgs& a, const Launch& l) {
     constexpr int V = Pieces<T, A>::V;
     const unsigned grid = a.slots * (unsigned)a.blocks;
     const size_t red = red_bytes(a, V), groups = sizeof(float2) * std::min(a.G, a.nv * V);    // at most 16 KB each
-    auto go = [&](auto tag, unsigned ctas, size_t smem, bool second) {
+    enum Mode { kPlain, kEarly, kCooperative };
+    auto go = [&](auto tag, unsigned ctas, size_t smem, Mode mode) {
         constexpr auto kernel = decltype(tag)::value;
         if (!allow_smem<kernel>(l.device)) return false;
-        cudaLaunchAttribute early = {};
-        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        early.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchAttribute attr = {};
+        if (mode == kCooperative) {
+            attr.id = cudaLaunchAttributeCooperative;
+            attr.val.cooperative = 1;
+        } else {
+            attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr.val.programmaticStreamSerializationAllowed = 1;
+        }
         cudaLaunchConfig_t config = {};
         config.gridDim = dim3(ctas);
         config.blockDim = dim3(kThreads);
         config.dynamicSmemBytes = smem;
         config.stream = l.st;
-        config.attrs = &early;
-        config.numAttrs = second ? 1 : 0;
+        config.attrs = &attr;
+        config.numAttrs = mode == kPlain ? 0 : 1;
+        if (cudaLaunchKernelEx(&config, kernel, a) != cudaSuccess) return false;
         note_launch();
-        return cudaLaunchKernelEx(&config, kernel, a) == cudaSuccess;
+        return true;
     };
     if (l.grad) {
         const size_t ring = Rows<T, A, 2, kGradStages>::kBytes;
-        return go(Kernel<k_norm_grad_sums<T, A, ACT>>(), grid, red + ring, false) &&
-               go(Kernel<k_norm_grad_apply<T, A, ACT>>(), grid + (unsigned)cdiv(a.C, 32), std::max(ring + groups, sizeof(double2) * kThreads), true);
+        return go(Kernel<k_norm_grad_sums<T, A, ACT>>(), grid, red + ring, kPlain) &&
+               go(Kernel<k_norm_grad_apply<T, A, ACT>>(), grid + (unsigned)cdiv(a.C, 32), std::max(ring + groups, sizeof(double2) * kThreads), kEarly);
+    }
+    if constexpr (Rows<T, A, 1, kStages>::kRing) {
+        if (l.kept) {
+            if (go(Kernel<k_norm_kept<T, A, ACT>>(), grid, Rows<T, A, 1, kKeptRows>::kBytes + std::max(red, groups), kCooperative))
+                return true;
+            // fewer SMs than the device has (a partition of it): the two launches do the same
+            if (cudaGetLastError() != cudaErrorCooperativeLaunchTooLarge) return false;
+        }
     }
     const size_t ring = Rows<T, A, 1, kStages>::kBytes;
-    return go(Kernel<k_norm_stats<T, A>>(), grid, red + ring, false) && go(Kernel<k_norm_apply<T, A, ACT>>(), grid, ring + groups, true);
+    return go(Kernel<k_norm_stats<T, A>>(), grid, red + ring, kPlain) && go(Kernel<k_norm_apply<T, A, ACT>>(), grid, ring + groups, kEarly);
 }
 
 template <typename T, int A>
@@ -849,8 +929,8 @@ bool launch_type(const NormArgs& a, const Launch& l) {
     return launch_chunk<T, 1>(a, l);
 }
 
-// Column blocks and tiles of a call.
-void shape(NormArgs& a, int V, int chunk, int ctas) {
+// Column blocks and tiles of a call; true where all rows can be kept on the SMs.
+bool shape(NormArgs& a, int V, int chunk, int sms, int per_sm, bool may_keep) {
     a.nvt = (int32_t)cdiv(a.C, V);
     // vectors per block: at least kBlockBytes of a row in a round of chunks, the narrowest that keeps nine tenths of the threads on vectors
     const int least = std::min(a.nvt, kBlockBytes / chunk);
@@ -874,9 +954,18 @@ void shape(NormArgs& a, int V, int chunk, int ctas) {
     // not for so many tiles that adding up their sums, which every CTA of the second pass does, takes long
     const int groups = std::min(a.G, (a.nv * V + a.width - 2) / a.width + 1);
     const int64_t most = std::max<int64_t>(kTilesPerLane * merge_lanes(groups), kMinTiles);
-    const int64_t tiles = std::min(most, (int64_t)std::max(1, ctas / a.blocks));
+    const size_t kept_smem = (size_t)kKeptRows * kThreads * kVecBytes + std::max(red_bytes(a, V), sizeof(float2) * a.nv * V);
+    const int64_t kept_ctas = std::min<int64_t>(kKeptCtas, 227 * 1024 / (kept_smem + 1024)) * sms;
+    const int64_t room = std::min(most, kept_ctas / a.blocks - a.B);      // slots: tiles and one for each sequence
+    if (may_keep && room > 0 && cdiv(cdiv(a.N, room), a.rl) <= kKeptRows) {
+        a.R = (uint32_t)(a.rl * cdiv(cdiv(a.N, room), a.rl));
+        a.slots = (uint32_t)(a.N / a.R + a.B);
+        return true;
+    }
+    const int64_t tiles = std::min(most, (int64_t)std::max(1, per_sm * sms / a.blocks));
     a.R = (uint32_t)(a.rl * std::min<int64_t>(kRowsPerThread, cdiv(cdiv(a.N, tiles), a.rl)));
     a.slots = (uint32_t)(a.N / a.R + a.B);
+    return false;
 }
 
 struct Call {
@@ -933,7 +1022,7 @@ ssa_status_t run_norm(Plan* p, const Call& c, int32_t C, int32_t G, float eps, i
     a.eps = eps;
     const DeviceScope on(p->device);
     if (!on.ok) return SSA_ERR_CUDA;
-    shape(a, kVecBytes / (int)es, A * (int)es, (grad ? 2 : 4) * sm_count(p->device));
+    const bool kept = shape(a, kVecBytes / (int)es, A * (int)es, sm_count(p->device), grad ? 2 : 4, !grad && A * es >= 4);
     if ((int64_t)a.slots * a.blocks >= ((int64_t)1 << 30)) return SSA_ERR_UNSUPPORTED;
     // one buffer of the tiles' sums
     const int64_t n_group = (int64_t)a.slots * a.over * G, n_chan = grad ? (int64_t)a.slots * C : 0;
@@ -944,7 +1033,7 @@ ssa_status_t run_norm(Plan* p, const Call& c, int32_t C, int32_t G, float eps, i
     a.rstd = c.rstd;
     const char* name = grad ? "group_norm_backward" : "group_norm";
     ProfScope ps(name, st);
-    const Launch l = {grad, act, A, p->device, st};
+    const Launch l = {grad, act, A, p->device, kept, st};
     const bool ok = dt == SSA_F32    ? launch_type<float>(a, l)
                     : dt == SSA_BF16 ? launch_type<__nv_bfloat16>(a, l)
                                      : launch_type<__half>(a, l);
