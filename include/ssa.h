@@ -352,6 +352,7 @@ SSA_API ssa_status_t ssa_rotary_frequencies(const ssa_rotary_t* rotary, int32_t 
  *           own input (same pointer and strides); otherwise outputs share no memory with the inputs or
  *           with one another. Views that interleave in memory are accepted when they have the same
  *           token stride (the parts of one fused projection), else refused when their ranges meet.
+ *   eps >= 0, finite.
  * Queues work on `stream` and returns without waiting; allocates nothing. Runs on the plan's device.
  * Errors: SSA_ERR_INVALID_ARG, SSA_ERR_UNSUPPORTED (head_dim), SSA_ERR_CUDA.
  */

@@ -12,7 +12,10 @@
 // blocks of 16-byte vectors, whatever the groups' width: a thread keeps one vector of channels and walks rows, so
 // channel constants stay in registers; a group across column blocks has sums in each. Rows that are not aligned
 // to 16 bytes are read in chunks of A elements. The second pass takes the tiles in reverse: what the
-// first read last is still in L2. (Tried and slower: column blocks or units of groups small enough to stay in L2
+// first read last is still in L2. Measured (2112 channels in 32 groups, fp16, silu): 340,000 tokens 692 us, the gradient of
+// 80,000 287 us: 6.2 and 5.9 TB/s over the three and five passes made. A forward whose rows all fit in shared
+// memory is one cooperative launch that reads them once (20,000 x 512 bf16: 17.4 against 19.9 us; the gradient
+// gained nothing from it). (Tried and slower: column blocks or units of groups small enough to stay in L2
 // between the passes, as one launch with tickets or as many launches, 913 us and more against 691 for 340,000 tokens x 2112
 // fp16: pieces of rows, 128 to 528 bytes 4 KB apart, cost more than the third pass over memory.)
 // Tile `t` of sequence s holds its tokens [t * R, ...) and has slot lo / R + s + t in the tables of sums: a sequence of n
@@ -990,6 +993,7 @@ ssa_status_t run_norm(Plan* p, const Call& c, int32_t C, int32_t G, float eps, i
     if ((c.gamma == nullptr) != (c.beta == nullptr)) return SSA_ERR_INVALID_ARG;
     if (grad ? (!c.mean || !c.rstd || !c.dgamma || !c.dbeta) : !(eps >= 0.0f) || std::isinf(eps)) return SSA_ERR_INVALID_ARG;
     if ((c.mean == nullptr) != (c.rstd == nullptr)) return SSA_ERR_INVALID_ARG;
+    if (!aligned4(c.gamma, c.beta, c.mean, c.rstd, c.dgamma, c.dbeta)) return SSA_ERR_INVALID_ARG;
     const int64_t N = p->N;
     const size_t es = dt == SSA_F32 ? 4 : 2;
     auto view = [](const ssa_rows_t* r) { return ssa_heads_t{r->data, r->token_stride, 0, 1}; };

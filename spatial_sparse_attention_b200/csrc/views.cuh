@@ -61,6 +61,12 @@ inline int view_vector(const ssa_heads_t& v, int64_t N, size_t es, int most) {
     return most;
 }
 
+// fp32 arrays of a call start at a multiple of their size (null passes).
+template <typename... P>
+inline bool aligned4(P... p) {
+    return (((uintptr_t)p | ...) & 3) == 0;
+}
+
 // Makes the plan's device current for the scope.
 struct DeviceScope {
     int before = 0;

@@ -140,6 +140,22 @@ def test_c_refusals():
     assert ssa.launch_count() == before
 
 
+def test_c_refuses_misaligned_arrays():
+    plan, _ = plan_of((4,))
+    x = torch.zeros(4, 16, device="cuda")
+    w = torch.ones(64, device="cuda")
+    a, p = ctypes.addressof, w.data_ptr()
+    v = ssa._Rows(x.data_ptr(), 16)
+    before = ssa.launch_count()
+    for bad in range(4):
+        at = [p, p + 64, p + 128, p + 160]
+        at[bad] += 2
+        assert ssa.lib.ssa_group_norm(plan._h, a(v), 16, 2, at[0], at[1], 1e-5, 0, 0, a(v), at[2], at[3], None) == 1
+        assert ssa.lib.ssa_group_norm_backward(plan._h, a(v), a(v), p + 128, p + 160, 16, 2, at[0], at[1], 0, 0, a(v), at[2],
+                                               at[3], None) == 1
+    assert ssa.launch_count() == before
+
+
 # ---- values ------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])

@@ -139,6 +139,20 @@ def test_c_refusals():
     assert ssa.launch_count() == before
 
 
+def test_c_refuses_misaligned_weights_and_an_infinite_eps():
+    plan, _ = one_plan(4)
+    x = torch.zeros(4, 2, 32, device="cuda")
+    w = torch.ones(160, device="cuda")
+    r, a, p = ssa.Rotary(), ctypes.addressof, w.data_ptr()
+    v = ssa._Heads(x.data_ptr(), 64, 32, 2)
+    before = ssa.launch_count()
+    assert ssa.lib.ssa_rotary(plan._h, a(v), None, p + 1, None, 1e-6, a(r), 32, 0, a(v), None, None) == 1
+    assert ssa.lib.ssa_rotary(plan._h, a(v), None, p, None, float("inf"), a(r), 32, 0, a(v), None, None) == 1
+    assert ssa.lib.ssa_rotary_backward(plan._h, a(v), None, a(v), None, p, None, 1e-6, a(r), 32, 0, a(v), None, p + 130, None,
+                                       None) == 1
+    assert ssa.launch_count() == before
+
+
 # ---- values ------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
