@@ -37,7 +37,7 @@ constexpr int kVecBytes = 16;
 constexpr int kMaxChannels = 65536;
 // Rows per thread of a full tile. The variance of a thread's rows comes from sums about its first row: with n rows
 // the cancellation is at most a factor n, as the pivot is one of them (sq <= n D^2, D the largest deviation from it, and
-// the squared deviations from the mean are at least D^2 / 2).
+// the squared deviations from the mean are at least D^2 / 2). The merges after that take deviations from means.
 constexpr int kRowsPerThread = 48;
 constexpr int kTilesPerLane = 10;       // tiles of a column that one lane of a merge adds up,
 constexpr int kMinTiles = 148;          // where that does not leave SMs without work
@@ -461,38 +461,42 @@ __device__ __forceinline__ void sum_tile(const NormArgs& a, const Block& b, cons
         for (int j = 0; j < V; ++j) mine[b.relative<A>(j)] = make_float2(fmaf(sum[j], inv, -p[j]), sq[j] - sum[j] * sum[j] * inv);
     }
     __syncthreads();
-    // the channels' row lanes into row 0, then the groups' channels
+    // the channels' row lanes into row 0, then the groups' channels: the mean first, then the deviations from it, as one
+    // lane or channel far from the others would cancel in a variance about it by their number (up to 256 and 512). What the
+    // mean is off by comes back as the deviations' sum.
     const int less = n / a.rl, more = n - less * a.rl, lanes = min(a.rl, n);    // rows per lane; lanes with one more
+    const float inv_n = 1.0f / (float)n;
     for_channels(a, b, [&](int c, bool valid, int q, int Q) {
         const float first = red[c].x;
-        float sum = 0.0f, sq = 0.0f;
+        float sum = 0.0f, rest = 0.0f, sq = 0.0f;
+        for (int l = q; l < lanes; l += Q) sum = fmaf(l < more ? less + 1.0f : (float)less, red[l * row_c + c].x - first, sum);
+        const float mean = fmaf(lane_sum(sum, Q), inv_n, first);
         for (int l = q; l < lanes; l += Q) {
             const float2 v = red[l * row_c + c];
-            const float k = l < more ? less + 1.0f : (float)less, d = v.x - first;
-            sum = fmaf(k, d, sum);
+            const float k = l < more ? less + 1.0f : (float)less, d = v.x - mean;
+            rest = fmaf(k, d, rest);
             sq += fmaf(k * d, d, v.y);
         }
-        sum = lane_sum(sum, Q);
+        rest = lane_sum(rest, Q);
         sq = lane_sum(sq, Q);
-        const float inv = 1.0f / (float)n;
-        if (q == 0 && valid) red[c] = make_float2(fmaf(sum, inv, first), sq - sum * sum * inv);
+        __syncwarp();       // row 0 is read by all lanes of the channel
+        if (q == 0 && valid) red[c] = make_float2(fmaf(rest, inv_n, mean), sq);
     });
     __syncthreads();
     for_groups(a, b, [&](int g, int lo, int hi, int l, int L) {
-        const float first = lo < hi ? red[lo].x : 0.0f;
-        float sum = 0.0f, sq = 0.0f;
+        const float first = lo < hi ? red[lo].x : 0.0f, inv = lo < hi ? 1.0f / (float)(hi - lo) : 0.0f;
+        float sum = 0.0f, rest = 0.0f, sq = 0.0f;
+        for (int c = lo + l; c < hi; c += L) sum += red[c].x - first;
+        const float mean = fmaf(lane_sum(sum, L), inv, first);
         for (int c = lo + l; c < hi; c += L) {
-            const float d = red[c].x - first;
-            sum += d;
+            const float d = red[c].x - mean;
+            rest += d;
             sq += fmaf(n * d, d, red[c].y);
         }
-        sum = lane_sum(sum, L);
+        rest = lane_sum(rest, L);
         sq = lane_sum(sq, L);
-        if (l == 0 && lo < hi) {
-            const float d = sum / (float)(hi - lo);
-            a.group_part[((int64_t)slot * a.over + b.index - first_block(a, g, V)) * a.G + g] =
-                make_float2(first + d, sq - n * sum * d);
-        }
+        if (l == 0 && lo < hi)
+            a.group_part[((int64_t)slot * a.over + b.index - first_block(a, g, V)) * a.G + g] = make_float2(fmaf(rest, inv, mean), sq);
     });
 }
 
