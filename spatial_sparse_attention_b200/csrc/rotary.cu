@@ -31,13 +31,14 @@ constexpr int kLane = 32;         // bytes of a row per lane
 constexpr int kStages = 3;        // rows per lane in flight or in use, forward
 constexpr int kStagedBelow = 2;   // half layout: loads of at most this many elements are staged
 constexpr int kGradStages = 3;    // gradient (two rows each)
+constexpr int kChain = 32;        // rows that a lane adds up in fp32 before the sums go on in fp64
 
 struct RowsArg {
     const void* x;        // forward: input; gradient: the forward's input (weights) or unused
     const void* g;        // gradient: gradient of the output
     void* out;
     const float* gamma;
-    float* part;          // gradient with weights: [CTAs of this tensor][D] partial sums
+    double* part;         // gradient with weights: [CTAs of this tensor][D] partial sums
     int64_t x_ts, x_hs, g_ts, g_hs, o_ts, o_hs;
     int32_t H;
     int32_t tile;         // gradient: tokens per tile
@@ -427,8 +428,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_rotary(const __grid_constant__ 
 }
 
 // The gradient with weights. Persistent: a CTA walks tiles of its tensor, its loads running ahead into the
-// next tile, and keeps the weights' sums of its lanes' channels in registers; it adds them up over its rows in a
-// fixed order at the end.
+// next tile, and keeps the weights' sums of its lanes' channels in registers, from which every kChain rows they go to fp64
+// sums in the lane's own places in shared memory (no barrier): a sum of millions of rows loses nothing to its length.
+// The CTA adds them up over its rows in a fixed order at the end.
 template <typename T, int V, bool HALF, int LANES, bool STAGED>
 __global__ void __launch_bounds__(kThreads, 2) k_rotary_grad(const __grid_constant__ RotArgs a) {
     using CUT = Cut<T, V, HALF>;
@@ -438,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_rotary_grad(const __grid_consta
     float* cs = (float*)(smem + 2 * S * stage_bytes(STAGED));
     float* sn = cs + a.tile * tab_stride(a.D);
     float* gamma = sn + a.tile * tab_stride(a.D);
+    double* sums64 = (double*)(gamma + a.D);    // [E][kThreads]
     const int which = blockIdx.x < a.ctas0 ? 0 : 1;
     const RowsArg& t = a.t[which];
     const int cta = blockIdx.x - (which ? a.ctas0 : 0), nctas = which ? gridDim.x - a.ctas0 : a.ctas0;
@@ -448,7 +451,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_rotary_grad(const __grid_consta
     lane_offsets<T, V, HALF>(a, G, l, off);
     float acc[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < E; ++i) {
+        acc[i] = 0.0f;
+        sums64[i * kThreads + threadIdx.x] = 0.0;
+    }
+    int chain = 0;
+    auto flush = [&] {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            sums64[i * kThreads + threadIdx.x] += (double)acc[i];
+            acc[i] = 0.0f;
+        }
+        chain = 0;
+    };
     const int H = t.H, step = kWarps * rpw, dt = step / H, dh = step - dt * H;
     const int r0 = (threadIdx.x >> 5) * rpw;
     const Cursor first = {r0 + sub, (r0 + sub) / H, (r0 + sub) % H};
@@ -531,40 +546,37 @@ __global__ void __launch_bounds__(kThreads, 2) k_rotary_grad(const __grid_consta
             }
             if (STAGED) __syncwarp();
             if (mine) slot.write(out + at.t * t.o_ts + at.h * t.o_hs, off, d);
+            if (++chain == kChain) flush();
             at.advance(step, dt, dh, H);
             stage = (stage + 1) % S;
         }
     }
-    // every lane's sums to shared memory; then one thread per element adds those of all warps and rows
-    cp_wait<0>();
-    __syncthreads();
-    float* red = (float*)smem;
-#pragma unroll
-    for (int i = 0; i < E; ++i) red[i * kThreads + threadIdx.x] = acc[i];
+    // one thread per element adds the sums of all warps and rows
+    flush();
     __syncthreads();
     if (threadIdx.x < a.D) {    // D = G * E
         const int i = threadIdx.x / G, ll = threadIdx.x - i * G;   // element i of lane ll
-        float s = 0.0f;
+        double s = 0.0;
         for (int w = 0; w < kWarps; ++w)
-            for (int q = 0; q < rpw; ++q) s += red[i * kThreads + w * 32 + q * G + ll];
+            for (int q = 0; q < rpw; ++q) s += sums64[i * kThreads + w * 32 + q * G + ll];
         t.part[(int64_t)cta * a.D + lane_channel<T, V, HALF>(a, G, ll, i)] = s;
     }
 }
 
 // dgamma[c] = sum over CTAs of part[cta][c], 32 channels per CTA, in a fixed order.
-__global__ void __launch_bounds__(1024) k_rotary_dgamma(const float* __restrict__ part0, const float* __restrict__ part1,
+__global__ void __launch_bounds__(1024) k_rotary_dgamma(const double* __restrict__ part0, const double* __restrict__ part1,
                                                         int n0, int n1, int D, float* out0, float* out1) {
-    __shared__ float red[32][33];
-    const float* part = blockIdx.y ? part1 : part0;
+    __shared__ double red[32][33];
+    const double* part = blockIdx.y ? part1 : part0;
     const int n = blockIdx.y ? n1 : n0, c = blockIdx.x * 32 + threadIdx.x;
-    float s = 0.0f;
+    double s = 0.0;
     for (int i = threadIdx.y; i < n; i += 32) s += part[(int64_t)i * D + c];
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0) {
-        s = 0.0f;
+        s = 0.0;
         for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
-        (blockIdx.y ? out1 : out0)[c] = s;
+        (blockIdx.y ? out1 : out0)[c] = (float)s;
     }
 }
 
@@ -627,7 +639,8 @@ bool launch_one(const RotArgs& a, unsigned grid, size_t smem, cudaStream_t st) {
 template <typename T, int V, bool HALF, int LANES, bool STAGED>
 bool launch_lanes(const RotArgs& a, unsigned grid, bool grad, cudaStream_t st) {
     const size_t ring = stage_bytes(STAGED), tables = sizeof(float) * 2 * ((size_t)a.tile * tab_stride(a.D) + a.D);
-    if (grad) return launch_one<k_rotary_grad<T, V, HALF, LANES, STAGED>>(a, grid, 2 * kGradStages * ring + tables, st);
+    const size_t sums64 = sizeof(double) * Cut<T, V, HALF>::E * kThreads;
+    if (grad) return launch_one<k_rotary_grad<T, V, HALF, LANES, STAGED>>(a, grid, 2 * kGradStages * ring + tables + sums64, st);
     if (a.t[0].gamma) return launch_one<k_rotary<T, V, HALF, true, LANES, STAGED>>(a, grid, kStages * ring + tables, st);
     return launch_one<k_rotary<T, V, HALF, false, LANES, STAGED>>(a, grid, kStages * ring + tables, st);
 }
@@ -782,7 +795,7 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
         const int64_t most = 2 * sms, hq = a.t[0].H, hk = a.t[1].H;
         const int n0 = (int)std::min(cdiv(N, a.t[0].tile), std::max<int64_t>(1, most * hq / (hq + hk)));
         const int n1 = nt == 2 ? (int)std::min(cdiv(N, a.t[1].tile), std::max<int64_t>(1, most * hk / (hq + hk))) : 0;
-        float* part = (float*)p->alloc(sizeof(float) * (size_t)(n0 + n1) * D, st, p->alloc_ctx);
+        double* part = (double*)p->alloc(sizeof(double) * (size_t)(n0 + n1) * D, st, p->alloc_ctx);
         if (!part) {
             out = SSA_ERR_ALLOC;
         } else {
