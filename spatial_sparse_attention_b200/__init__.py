@@ -90,7 +90,7 @@ class Rotary(ctypes.Structure):
     theta: base. layout: "interleaved" (pairs (2p, 2p+1)) or "half" (pairs (p, p + dim/2)). dim: rotated
     channels (None = the whole head). scaling: "none", "linear", "ntk" or "yarn", for a grid `scale`
     times the trained one; extent: the trained extent, with beta_slow and beta_fast, for yarn. mscale: factor on
-    the rotated channels (None = 1, for yarn 0.1 ln(scale) + 1)."""
+    the rotated channels (None = 1, for yarn with scale > 1 0.1 ln(scale) + 1)."""
     _fields_ = [("theta", ctypes.c_double), ("scale", ctypes.c_double), ("extent", ctypes.c_double),
                 ("beta_slow", ctypes.c_double), ("beta_fast", ctypes.c_double), ("mscale", ctypes.c_float),
                 ("dim", _i32), ("layout", _i32), ("scaling", _i32)]
@@ -105,7 +105,7 @@ class Rotary(ctypes.Structure):
         if dim is not None and dim < 1:
             raise ValueError("dim must be positive (None = the whole head)")
         if mscale is None:
-            mscale = 0.1 * math.log(scale) + 1.0 if scaling == "yarn" and scale > 0 else 1.0
+            mscale = 0.1 * math.log(scale) + 1.0 if scaling == "yarn" and scale > 1 else 1.0
         super().__init__(theta, scale, extent, beta_slow, beta_fast, mscale, dim or 0, _LAYOUT[layout],
                          _SCALING[scaling])
 
