@@ -364,7 +364,7 @@ SSA_API ssa_status_t ssa_rotary(ssa_plan_t plan, const ssa_heads_t* q, const ssa
 /*
  * Gradients of ssa_rotary: from dq_out, dk_out (with respect to its outputs) to dq, dk (its inputs)
  * and, when the weights are set, dq_gamma, dk_gamma (device fp32 [head_dim] each, sums over all tokens and
- * heads; written, not added to). q and k are the forward's inputs and are read only when the weights are
+ * heads; written, not added to; the two share no memory). q and k are the forward's inputs and are read only when the weights are
  * set (else they may be NULL). k-side pointers all NULL: queries only. dq and dk may be dq_out and dk_out
  * themselves (or q and k); otherwise as the outputs of ssa_rotary. Fixed summation order: equal inputs, alignment
  * included, give equal bits. Partial sums go to a buffer that is allocated and freed stream-ordered through the
@@ -395,7 +395,8 @@ typedef enum { SSA_ACT_NONE = 0, SSA_ACT_SILU = 1, SSA_ACT_GELU = 2 } ssa_activa
  * act: none, silu z / (1 + exp(-z)), or gelu z * Phi(z) (the normal distribution function, not its tanh form).
  *   gamma, beta: device fp32 [channels], both or (NULL) neither (1 and 0).
  *   y: output; may be x itself (same pointer and stride), otherwise shares no memory with x.
- *   mean, rstd: outputs, device fp32 [B, groups], both or (NULL) neither; 0 for a sequence without tokens.
+ *   mean, rstd: outputs, device fp32 [B, groups], both or (NULL) neither; 0 for a sequence without tokens. They share
+ *           no memory with one another, nor with other arrays of the call.
  * fp32 arithmetic, statistics merged in fp64, one rounding to the type at the end; the variance comes from
  * deviations, not from a difference of large sums. Fixed summation order: equal inputs, alignment included, give equal
  * bits. Strides >= 0 (y: >= channels). Queues work on `stream` and returns without waiting; partial sums go to a buffer that
@@ -410,8 +411,8 @@ SSA_API ssa_status_t ssa_group_norm(ssa_plan_t plan, const ssa_rows_t* x, int32_
 /*
  * Gradients of ssa_group_norm: from dy (with respect to y), its input x and its mean and rstd to dx, dgamma and
  * dbeta (device fp32 [channels], sums over all tokens; written, not added to; also without weights, as if they
- * were 1 and 0). dx may be dy itself or x itself; otherwise it shares no memory with them. Otherwise as
- * ssa_group_norm.
+ * were 1 and 0). dx may be dy itself or x itself; otherwise it shares no memory with them. dgamma and dbeta share no
+ * memory with one another, nor with other arrays of the call. Otherwise as ssa_group_norm.
  */
 SSA_API ssa_status_t ssa_group_norm_backward(ssa_plan_t plan, const ssa_rows_t* dy, const ssa_rows_t* x,
                                              const float* mean, const float* rstd, int32_t channels,

@@ -998,6 +998,13 @@ ssa_status_t run_norm(Plan* p, const Call& c, int32_t C, int32_t G, float eps, i
     if (grad ? (!c.mean || !c.rstd || !c.dgamma || !c.dbeta) : !(eps >= 0.0f) || std::isinf(eps)) return SSA_ERR_INVALID_ARG;
     if ((c.mean == nullptr) != (c.rstd == nullptr)) return SSA_ERR_INVALID_ARG;
     if (!aligned4(c.gamma, c.beta, c.mean, c.rstd, c.dgamma, c.dbeta)) return SSA_ERR_INVALID_ARG;
+    // the pass that writes reads the weights (and the gradient's the statistics) while other CTAs of it write these
+    const int64_t stats = (int64_t)p->B * G;
+    const Span gamma = {c.gamma, C}, beta = {c.beta, C}, mean = {c.mean, stats}, rstd = {c.rstd, stats};
+    const Span outs[2] = {grad ? Span{c.dgamma, C} : mean, grad ? Span{c.dbeta, C} : rstd};
+    if (!apart(outs[0], outs[1])) return SSA_ERR_INVALID_ARG;
+    for (const Span& o : outs)
+        if (!apart(o, gamma) || !apart(o, beta) || (grad && (!apart(o, mean) || !apart(o, rstd)))) return SSA_ERR_INVALID_ARG;
     const int64_t N = p->N;
     const size_t es = dt == SSA_F32 ? 4 : 2;
     auto view = [](const ssa_rows_t* r) { return ssa_heads_t{r->data, r->token_stride, 0, 1}; };

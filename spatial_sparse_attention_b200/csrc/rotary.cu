@@ -726,6 +726,7 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
             if (in[j] && !(j / 2 == i && same_view(*c.out[i], *in[j], N)) && !disjoint(*c.out[i], *in[j], N, D, es))
                 return SSA_ERR_INVALID_ARG;
     if (nt == 2 && !disjoint(*c.out[0], *c.out[1], N, D, es)) return SSA_ERR_INVALID_ARG;
+    if (nt == 2 && !apart({c.dgamma[0], D}, {c.dgamma[1], D})) return SSA_ERR_INVALID_ARG;
 
     RotArgs a = {};
     int32_t axis[kMaxPairs];

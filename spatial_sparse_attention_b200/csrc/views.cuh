@@ -67,6 +67,16 @@ inline bool aligned4(P... p) {
     return (((uintptr_t)p | ...) & 3) == 0;
 }
 
+// Whether fp32 arrays share no memory (null: no array).
+struct Span {
+    const float* p;
+    int64_t n;
+};
+inline bool apart(const Span& a, const Span& b) {
+    const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+    return !a.p || !b.p || pa + 4 * (uintptr_t)a.n <= pb || pb + 4 * (uintptr_t)b.n <= pa;
+}
+
 // Makes the plan's device current for the scope.
 struct DeviceScope {
     int before = 0;
