@@ -13,7 +13,7 @@
 // registers), several rows ahead. The cosines and sines are shared by all heads of a token: a CTA takes a
 // tile of tokens, queries and keys, and computes them once into shared memory while its first loads fly.
 // Measured (fp16, 44 heads x 96): 110,000 tokens 302 us, 6.2 TB/s; the gradient with weights of 80,000 tokens
-// 343 us, 5.9 TB/s; a plain copy reaches 6.55. What is next to memory is instruction issue.
+// 350 us, 5.8 TB/s; a plain copy reaches 6.55. What is next to memory is instruction issue.
 #include <algorithm>
 #include <cmath>
 
@@ -31,7 +31,9 @@ constexpr int kLane = 32;         // bytes of a row per lane
 constexpr int kStages = 3;        // rows per lane in flight or in use, forward
 constexpr int kStagedBelow = 2;   // half layout: loads of at most this many elements are staged
 constexpr int kGradStages = 3;    // gradient (two rows each)
-constexpr int kChain = 32;        // rows that a lane adds up in fp32 before the sums go on in fp64
+// Rows that a lane adds up in fp32 before the sums go on in fp64. Gradient of 80,000 tokens x 44 heads x 96 fp16: 342 us without,
+// 345 every 128 rows, 350 every 32; the sums of equal terms, whose roundings point one way, are off by up to 30 and 8 units of 2^-24.
+constexpr int kChain = 32;
 
 struct RowsArg {
     const void* x;        // forward: input; gradient: the forward's input (weights) or unused
@@ -506,49 +508,53 @@ __global__ void __launch_bounds__(kThreads, 2) k_rotary_grad(const __grid_consta
         const int nrow = ntok * H;
         Cursor at = first;
         T* out = (T*)t.out + tok0 * t.o_ts;
-        for (int w0 = 0; w0 < nrow; w0 += step) {
-            fetch((stage + S - 1) % S);
-            cp_wait<S - 1>();
-            const bool mine = at.r < nrow && sub < rpw;
-            float e[E], d[E], sums[2] = {0.0f, 0.0f};   // sum x^2, sum du gamma x
-            const Slot<T, CUT, STAGED> slot(ring_g, stage, sub, l, G);
-            if (STAGED) __syncwarp();
-            if (mine) {
-                Slot<T, CUT, STAGED>(smem, stage, sub, l, G).read(off, e);
-                slot.read(off, d);
-                const int tab = at.t * tab_stride(a.D);
-                turn_row<CUT>(d, cs + tab, sn + tab, l, G, a.pairs);
-                float odd0 = 0.0f, odd1 = 0.0f;
+        for (int from = 0; from < nrow; from += kChain * step) {
+            const int to = min(nrow, from + kChain * step), rows = (to - from + step - 1) / step;
+            if (chain + rows > kChain) flush();
+            chain += rows;
+            for (int w0 = from; w0 < to; w0 += step) {
+                fetch((stage + S - 1) % S);
+                cp_wait<S - 1>();
+                const bool mine = at.r < nrow && sub < rpw;
+                float e[E], d[E], sums[2] = {0.0f, 0.0f};   // sum x^2, sum du gamma x
+                const Slot<T, CUT, STAGED> slot(ring_g, stage, sub, l, G);
+                if (STAGED) __syncwarp();
+                if (mine) {
+                    Slot<T, CUT, STAGED>(smem, stage, sub, l, G).read(off, e);
+                    slot.read(off, d);
+                    const int tab = at.t * tab_stride(a.D);
+                    turn_row<CUT>(d, cs + tab, sn + tab, l, G, a.pairs);
+                    float odd0 = 0.0f, odd1 = 0.0f;
 #pragma unroll
-                for (int i = 0; i < E; i += 2) {
-                    float g0, g1;
-                    mul2(g0, g1, d[i], d[i + 1], gam[i], gam[i + 1]);
-                    fma2(sums[0], odd0, e[i], e[i + 1], e[i], e[i + 1], sums[0], odd0);
-                    fma2(sums[1], odd1, g0, g1, e[i], e[i + 1], sums[1], odd1);
+                    for (int i = 0; i < E; i += 2) {
+                        float g0, g1;
+                        mul2(g0, g1, d[i], d[i + 1], gam[i], gam[i + 1]);
+                        fma2(sums[0], odd0, e[i], e[i + 1], e[i], e[i + 1], sums[0], odd0);
+                        fma2(sums[1], odd1, g0, g1, e[i], e[i + 1], sums[1], odd1);
+                    }
+                    sums[0] += odd0;
+                    sums[1] += odd1;
                 }
-                sums[0] += odd0;
-                sums[1] += odd1;
-            }
-            row_sum(sums, G, base, l);
-            if (mine) {
-                const float inv = rsqrtf(fmaf(sums[0], a.inv_d, a.eps));
-                const float dot = -sums[1] * inv * a.inv_d;      // - mean of g n
+                row_sum(sums, G, base, l);
+                if (mine) {
+                    const float inv = rsqrtf(fmaf(sums[0], a.inv_d, a.eps));
+                    const float dot = -sums[1] * inv * a.inv_d;      // - mean of g n
 #pragma unroll
-                for (int i = 0; i < E; i += 2) {
-                    float n0, n1;
-                    mul2(n0, n1, e[i], e[i + 1], inv, inv);
-                    fma2(acc[i], acc[i + 1], d[i], d[i + 1], n0, n1, acc[i], acc[i + 1]);
-                    mul2(d[i], d[i + 1], d[i], d[i + 1], gam[i], gam[i + 1]);
-                    fma2(d[i], d[i + 1], n0, n1, dot, dot, d[i], d[i + 1]);
-                    mul2(d[i], d[i + 1], d[i], d[i + 1], inv, inv);
+                    for (int i = 0; i < E; i += 2) {
+                        float n0, n1;
+                        mul2(n0, n1, e[i], e[i + 1], inv, inv);
+                        fma2(acc[i], acc[i + 1], d[i], d[i + 1], n0, n1, acc[i], acc[i + 1]);
+                        mul2(d[i], d[i + 1], d[i], d[i + 1], gam[i], gam[i + 1]);
+                        fma2(d[i], d[i + 1], n0, n1, dot, dot, d[i], d[i + 1]);
+                        mul2(d[i], d[i + 1], d[i], d[i + 1], inv, inv);
+                    }
+                    slot.put_back(off, d);
                 }
-                slot.put_back(off, d);
+                if (STAGED) __syncwarp();
+                if (mine) slot.write(out + at.t * t.o_ts + at.h * t.o_hs, off, d);
+                at.advance(step, dt, dh, H);
+                stage = (stage + 1) % S;
             }
-            if (STAGED) __syncwarp();
-            if (mine) slot.write(out + at.t * t.o_ts + at.h * t.o_hs, off, d);
-            if (++chain == kChain) flush();
-            at.advance(step, dt, dh, H);
-            stage = (stage + 1) % S;
         }
     }
     // one thread per element adds the sums of all warps and rows
