@@ -399,7 +399,8 @@ typedef enum { SSA_ACT_NONE = 0, SSA_ACT_SILU = 1, SSA_ACT_GELU = 2 } ssa_activa
  *           no memory with one another, nor with other arrays of the call.
  * fp32 arithmetic, statistics merged in fp64, one rounding to the type at the end; the variance comes from
  * deviations, not from a difference of large sums. Fixed summation order: equal inputs, alignment included, give equal
- * bits. Strides >= 0 (y: >= channels). Queues work on `stream` and returns without waiting; partial sums go to a buffer that
+ * bits. Strides >= 0 (y: >= channels). Inputs that fit in the device's shared memory take one cooperative launch, others
+ * two launches. Queues work on `stream` and returns without waiting; partial sums go to a buffer that
  * is allocated and freed stream-ordered through the allocator. Runs on the plan's device.
  * Errors: SSA_ERR_INVALID_ARG, SSA_ERR_UNSUPPORTED (more than 65536 channels), SSA_ERR_ALLOC, SSA_ERR_CUDA.
  */

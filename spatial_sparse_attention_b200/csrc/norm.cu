@@ -12,10 +12,11 @@
 // blocks of 16-byte vectors, whatever the groups' width: a thread keeps one vector of channels and walks rows, so
 // channel constants stay in registers; a group across column blocks has sums in each. Rows that are not aligned
 // to 16 bytes are read in chunks of A elements. The second pass takes the tiles in reverse: what the
-// first read last is still in L2. Measured (2112 channels in 32 groups, fp16, silu): 340,000 tokens 692 us, the gradient of
-// 80,000 287 us: 6.2 and 5.9 TB/s over the three and five passes made. A forward whose rows all fit in shared
-// memory is one cooperative launch that reads them once (20,000 x 512 bf16: 17.4 against 19.9 us; the gradient
-// gained nothing from it). (Tried and slower: column blocks or units of groups small enough to stay in L2
+// first read last is still in L2. Measured (2112 channels in 32 groups, fp16, silu): 340,000 tokens 699 us, the gradient of
+// 80,000 288 us: 6.2 and 5.9 TB/s over the three and five passes made. A forward whose rows all fit in shared
+// memory is one cooperative launch that reads them once (20,000 x 512 bf16: 18 against 21 us; the gradient
+// gained nothing from it).
+// Inside a tile sums are fp32 (at most 48 rows of a thread, then up to 256 threads and 680 channels), from tile to tile fp64. (Tried and slower: column blocks or units of groups small enough to stay in L2
 // between the passes, as one launch with tickets or as many launches, 913 us and more against 691 for 340,000 tokens x 2112
 // fp16: pieces of rows, 128 to 528 bytes 4 KB apart, cost more than the third pass over memory.)
 // Tile `t` of sequence s holds its tokens [t * R, ...) and has slot lo / R + s + t in the tables of sums: a sequence of n
@@ -340,7 +341,8 @@ __device__ __forceinline__ float ex2_scaled(float x, float hi, float lo) {
 }
 
 // sigma(z), by the hardware's exponential and reciprocal. For the 16-bit types the exponent's product is rounded
-// (2^-20 relative for |z| < 16, far below theirs); with expf and a division fp32 would wait for instructions, not memory.
+// (|z| 2^-24 relative, far below a step of theirs; the weights' fp32 gradients are sums of such terms, whose 16-bit inputs are
+// known to less than that); with expf and a division fp32 would wait for instructions, not memory.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float z) {
     if constexpr (sizeof(T) == 2) return rcp(1.0f + ex2(z * -1.4426950408889634f));
@@ -462,7 +464,7 @@ __device__ __forceinline__ void sum_tile(const NormArgs& a, const Block& b, cons
     }
     __syncthreads();
     // the channels' row lanes into row 0, then the groups' channels: the mean first, then the deviations from it, as one
-    // lane or channel far from the others would cancel in a variance about it by their number (up to 256 and 512). What the
+    // lane or channel far from the others would cancel in a variance about it by their number (up to 256 and 680). What the
     // mean is off by comes back as the deviations' sum.
     const int less = n / a.rl, more = n - less * a.rl, lanes = min(a.rl, n);    // rows per lane; lanes with one more
     const float inv_n = 1.0f / (float)n;
@@ -878,7 +880,7 @@ template <typename T, int A, int ACT>
 bool launch_act(const NormArgs& a, const Launch& l) {
     constexpr int V = Pieces<T, A>::V;
     const unsigned grid = a.slots * (unsigned)a.blocks;
-    const size_t red = red_bytes(a, V), groups = sizeof(float2) * std::min(a.G, a.nv * V);    // at most 16 KB each
+    const size_t red = red_bytes(a, V), groups = sizeof(float2) * std::min(a.G, a.nv * V);    // at most 32 and 16 KB
     enum Mode { kPlain, kEarly, kCooperative };
     auto go = [&](auto tag, unsigned ctas, size_t smem, Mode mode) {
         constexpr auto kernel = decltype(tag)::value;

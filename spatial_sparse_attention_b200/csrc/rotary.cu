@@ -12,7 +12,7 @@
 // lane's next rows are always in flight: they go to the lane's own places in shared memory (no barrier, no
 // registers), several rows ahead. The cosines and sines are shared by all heads of a token: a CTA takes a
 // tile of tokens, queries and keys, and computes them once into shared memory while its first loads fly.
-// Measured (fp16, 44 heads x 96): 110,000 tokens 302 us, 6.2 TB/s; the gradient with weights of 80,000 tokens
+// Measured (fp16, 44 heads x 96): 110,000 tokens 303 us, 6.1 TB/s; the gradient with weights of 80,000 tokens
 // 350 us, 5.8 TB/s; a plain copy reaches 6.55. What is next to memory is instruction issue.
 #include <algorithm>
 #include <cmath>
@@ -764,7 +764,7 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
     // loads of aligned rows, the rows go through shared memory whole
     int side = V;
     while (half && side > 1 && a.pairs % side) side >>= 1;
-    V = V == full && side <= kStagedBelow ? (side < full ? 0 : V) : side;
+    V = V == full && side <= kStagedBelow ? 0 : side;     // (kStagedBelow < full)
     a.coords = p->coords;
     a.N = N;
     a.D = D;

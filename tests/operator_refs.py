@@ -93,8 +93,9 @@ def rotary(x, coords, gamma=None, eps=1e-6, **opt):
     """(output, bound) of the forward for one of q, k."""
     D = x.shape[2]
     u = x if gamma is None else x / np.sqrt((x * x).mean(2, keepdims=True) + eps) * gamma
-    # normalisation: a sum of up to 16 + 4 terms and a division under a square root (11 u), rsqrtf
-    # (2 ulp, 4 u), two products; the angle (3 u), sincospif (2 ulp) and mscale, product and sum: 32 u covers them
+    # normalisation: a sum of squares in chains of at most 8 + 1 + 4 additions and the mean (14 u) under a square root (7 u),
+    # rsqrtf (2 ulp, 4 u), two products (2 u); cosine and sine by series of a 32-bit phase (the phase below 0.1 u, the remainder's
+    # rounding and product 1.5 u, the series 2 u) and mscale (2 u); product and sum (2 u): 21 u, 32 u covers them
     return rotate(u, coords, D, **opt), 32 * U * partner_magnitude(u, D, **opt)
 
 
@@ -139,15 +140,16 @@ def activation_grad(z, name):
 
 
 def activation_error(z, name):
-    """Bound, in units u, of the kernels' error of act(z) / |z| and of act'(z): sigma by a fast exponential
-    (2 + 1.2|z| ulp) and quotient (2 ulp); Phi to 5 ulp, the exponential of -z^2/2 to 2 ulp of itself and z^2 u of its
-    argument; a few operations on top. |act'| and its terms stay below 1.3 + |z|/4."""
+    """Bound, in units u, of the kernels' error of act(z) / |z| and of act'(z): sigma by the hardware's exponential
+    (2 ulp, 4 u, and |z| u of its rounded argument) and reciprocal (1 ulp, 2 u); Phi by a polynomial off by up to 6 u and its
+    evaluation (8 u), times the exponential of -z^2/2 (2 ulp and z^2 u of its argument) and a reciprocal; a few operations on top.
+    |act'| and its terms stay below 1.3 + |z|/4."""
     if name not in ("silu", "gelu"):
         return np.zeros_like(z)
     return (24 + 4 * np.abs(z) + 2 * np.minimum(z * z, 30)) * (1.3 + np.abs(z) / 4)
 
 
-DEPTH = 64 + 288 + 8    # longest chain of fp32 additions: rows of a thread, row lanes of a CTA, the merge
+DEPTH = 64 + 288 + 8    # covers the longest chain of fp32 additions: 48 rows of a thread, up to 256 row lanes of a CTA, the channels
 
 
 def norm_stats(x, cu, groups):
@@ -170,10 +172,11 @@ def _rows_of(table, cu, C):
 
 
 def group_norm(x, cu, groups, gamma=None, beta=None, eps=1e-5, act=None):
-    """(y, bound), (mean, bound), (rstd, bound). The kernels add deviations from a pivot among the values: the mean of
-    up to 64 of them is off by 64 u of their size, at most twice the largest deviation, plus 8 u of the values;
-    the variance by the cancellation of up to 64 terms, 2 (1 + 4) times 70 u (pivots of random rows are off
-    the mean by at most 4 variances on average)."""
+    """(y, bound), (mean, bound), (rstd, bound). The kernels add a thread's deviations from a pivot among its rows: the mean of
+    up to 48 of them is off by 50 u of their size, at most twice the largest deviation, plus 8 u of the values;
+    the variance by the cancellation of up to 48 terms, 2 (1 + 4) times 51 u (pivots of random rows are off
+    the mean by at most 4 variances on average). Row lanes and channels merge about their means: chains of at most 27 additions and 3 u
+    a term. 540 u of the variance, half of that of rstd: below 360 u."""
     C = x.shape[1]
     mean, var, size, most = norm_stats(x, cu, groups)
     empty = (np.diff(cu) == 0)[:, None] | np.zeros_like(mean, bool)
