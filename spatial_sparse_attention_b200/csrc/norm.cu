@@ -36,14 +36,19 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVecBytes = 16;
 constexpr int kMaxChannels = 65536;
-// Rows per thread of a full tile. The variance of a thread's rows comes from sums about its first row: with n rows
-// the cancellation is at most a factor n, as the pivot is one of them (sq <= n D^2, D the largest deviation from it, and
-// the squared deviations from the mean are at least D^2 / 2). The merges after that take deviations from means.
+// Rows per thread of a full tile.
 constexpr int kRowsPerThread = 48;
+// The variance of a thread's rows comes from sums about its first row, and after kSettled of them about those rows' mean. With n rows
+// the cancellation about one of them is at most a factor n (sq <= n D^2, D the largest deviation from it, and
+// the squared deviations from the mean are at least D^2 / 2); about the mean of n0 of n rows it is n / n0, as
+// what the others have in common off it counts n0 (n - n0) / n times in the variance. So a first row far from the others costs
+// a factor 8 in place of 48. The merges after that take deviations from means.
+constexpr int kSettled = 8;
 constexpr int kTilesPerLane = 10;       // tiles of a column that one lane of a merge adds up,
 constexpr int kMinTiles = 148;          // where that does not leave SMs without work
 constexpr int kBlockBytes = 128;        // of a row that a column block's threads read together, at least
 constexpr int kStages = 8;              // rows per thread in flight or in use: forward, gradient
+static_assert(kStages == kSettled, "the sums' pivot moves after the ring's first round");
 constexpr int kGradStages = 6;
 constexpr int kKeptRows = 12;           // rows per thread and CTAs per SM of the one-launch forward: 198 KB of 227
 constexpr int kKeptCtas = 3;
@@ -228,9 +233,10 @@ struct Rows {
             for (int i = 0; i < N; ++i) P::unpack(raw[i], i, e);
         }
     }
-    // f(e) for every row, e[k] being its vector of array k; f may write over the row (in place)
-    template <bool KEPT, typename F>
-    __device__ __forceinline__ void each(F f) {
+    // f(e) for every row, e[k] being its vector of array k; f may write over the row (in place). g() once after the first
+    // kSettled rows, where more follow (not for kept rows, which are few).
+    template <bool KEPT, typename F, typename Then>
+    __device__ __forceinline__ void each(F f, Then g) {
         float e[K][V];
         if constexpr (KEPT) {
 #pragma unroll 4
@@ -250,6 +256,9 @@ struct Rows {
                         for (int k = 0; k < K; ++k) read(j, k, e[k]);
                         f(e);
                     }
+                }
+                if constexpr (STAGES == kSettled) {
+                    if (i == 0 && count > kSettled) g();
                 }
             }
         } else {
@@ -277,8 +286,14 @@ struct Rows {
                         f(e);
                     }
                 }
+                static_assert(kSettled % U == 0, "the rows of a batch come before or after g");
+                if (i + U == kSettled && count > kSettled) g();
             }
         }
+    }
+    template <bool KEPT, typename F>
+    __device__ __forceinline__ void each(F f) {
+        each<KEPT>(f, [] {});
     }
 };
 
@@ -441,7 +456,7 @@ __device__ __forceinline__ void sum_tile(const NormArgs& a, const Block& b, cons
     const int n = tile.n, row_c = red_row(a, V), count = rows.count;
     const uint32_t slot = tile.slot;
     if (count) {
-        float p[V], sum[V], sq[V];      // p: the first row, negated
+        float p[V], sum[V], sq[V];      // p: the pivot, negated
         rows.template peek<KEPT>(p);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -455,6 +470,15 @@ __device__ __forceinline__ void sum_tile(const NormArgs& a, const Block& b, cons
                 add2(d0, d1, e[0][j], e[0][j + 1], p[j], p[j + 1]);
                 add2(sum[j], sum[j + 1], sum[j], sum[j + 1], d0, d1);
                 fma2(sq[j], sq[j + 1], d0, d1, d0, d1, sq[j], sq[j + 1]);
+            }
+        }, [&] {
+            // on about the mean of the rows so far: p moves by delta
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float to = fmaf(sum[j], -1.0f / kSettled, p[j]), delta = p[j] - to, rest = fmaf(-(float)kSettled, delta, sum[j]);
+                sq[j] = fmaf(-delta, sum[j] + rest, sq[j]);
+                sum[j] = rest;
+                p[j] = to;
             }
         });
         const float inv = 1.0f / (float)count;
@@ -509,8 +533,10 @@ __device__ __forceinline__ void write_empty(const NormArgs& a, const Block& b, c
             a.mean[(int64_t)tile.s * a.G + g] = a.rstd[(int64_t)tile.s * a.G + g] = 0.0f;
 }
 
+// Four CTAs per SM (64 registers); with 2-byte chunks three, whose batches of rows lie in registers (109,000 x 211 fp16: 86 us, with
+// two 94).
 template <typename T, int A>
-__global__ void __launch_bounds__(kThreads) k_norm_stats(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(kThreads, A * sizeof(T) == 2 ? 3 : 4) k_norm_stats(const __grid_constant__ NormArgs a) {
     constexpr int V = Pieces<T, A>::V;
     extern __shared__ __align__(16) char smem[];
     float2* red = (float2*)smem;        // [rl][red_row], then the ring
