@@ -1082,7 +1082,8 @@ ssa_status_t run_norm(Plan* p, const Call& c, int32_t C, int32_t G, float eps, i
                                      : launch_type<__half>(a, l);
     p->release(a.group_part, st, p->alloc_ctx);
     trace_step(name, st);
-    return ok && cudaGetLastError() == cudaSuccess ? SSA_OK : SSA_ERR_CUDA;
+    const bool clear = cudaGetLastError() == cudaSuccess;     // read in any case: the next call is not to find it
+    return ok && clear ? SSA_OK : SSA_ERR_CUDA;
 }
 
 }  // namespace

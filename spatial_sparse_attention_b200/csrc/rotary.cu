@@ -816,7 +816,8 @@ ssa_status_t run_rotary(Plan* p, const Call& c, float eps, const ssa_rotary_t* r
             p->release(part, st, p->alloc_ctx);
         }
     }
-    if (out == SSA_OK && cudaGetLastError() != cudaSuccess) out = SSA_ERR_CUDA;
+    const bool clear = cudaGetLastError() == cudaSuccess;     // read in any case: the next call is not to find it
+    if (out == SSA_OK && !clear) out = SSA_ERR_CUDA;
     trace_step(name, st);
     return out;
 }
