@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import operator_refs as ref
-from test_gpu_rotary import one_plan, rows, weights
+from test_gpu_rotary import check_backward, check_forward, one_plan, rows, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,24 @@ def test_equal_terms_over_many_rows(n, heads, keys, D, dtype):
         off = abs(ref.f64(outs[2 + i]) / want - 1)[2:]
         print(f"{'qk'[i]}: off by {off.max() / ref.U:.1f} u")
         assert off.max() <= 46 * ref.U
+
+
+@pytest.mark.parametrize("n,heads,keys,D,dtype", [(3, 65535, 7, 32, "f32"), (2, 5, 65535, 96, "f16"), (5, 3001, 2999, 128, "bf16")])
+def test_more_heads_than_a_tile_has_rows(n, heads, keys, D, dtype):
+    """Tiles of one token with thousands of rows a thread; the sums' chain of 32 is inside the tile. The weights' gradients at
+    a bound that does not grow with the rows: 96 u and the chain's 32 u of the terms' magnitudes."""
+    plan, c = one_plan(n, seed=n)
+    q, k = rows((n, heads, D), dtype, 1).cuda(), rows((n, keys, D), dtype, 2).cuda()
+    dq, dk = rows((n, heads, D), dtype, 3).cuda(), rows((n, keys, D), dtype, 4).cuda()
+    check_forward(plan, c, q, k, {}, weights(D, 5))
+    check_backward(plan, c, dq, dk, q, k, {}, weights(D, 5), depth=32)
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_large_shell_at_the_short_chains_bound(layout):
+    """Many tiles per CTA, its loads running on into the next tile, at the same bound."""
+    n, h = 60000, 22
+    plan, c = one_plan(n, edge=128, seed=1)
+    q, k = rows((n, h, 32), "f16", 1).cuda(), rows((n, 2, 32), "f16", 2).cuda()
+    dq, dk = rows((n, h, 32), "f16", 3).cuda(), rows((n, 2, 32), "f16", 4).cuda()
+    check_backward(plan, c, dq, dk, q, k, dict(layout=layout, dim=18), weights(32, 5), depth=32)
